@@ -1,0 +1,243 @@
+// C-ABI entry points of the dense operators around the expert layer (norm,
+// gated feed-forward block, optimiser step): host-side argument checks, then
+// the kernel launches.  No allocation, no host<->device copies, no sync, no
+// C++ exception leaves a call.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "dense_args.h"
+#include "moe.h"
+
+extern "C" {
+int moe_norm_backward_parts(int64_t);
+moe_status_t moe_add_rmsnorm_launch(const moe::NormArgs*, int, int, hipStream_t);
+moe_status_t moe_rmsnorm_backward_launch(const moe::NormBwdArgs*, int, int, float*, hipStream_t);
+size_t moe_gated_ffn_ws_impl(int64_t, int32_t, int32_t, int, int);
+moe_status_t moe_gated_ffn_launch(const uint16_t*, int64_t, const uint16_t*, const uint16_t*, const uint16_t*, int64_t,
+                                  int64_t, int32_t, int32_t, uint16_t*, uint16_t*, uint16_t*, void*, hipStream_t);
+size_t moe_gated_ffn_backward_ws_impl(void);
+moe_status_t moe_gated_ffn_backward_launch(const uint16_t*, const uint16_t*, const uint16_t*, const uint16_t*,
+                                           const uint16_t*, const uint16_t*, int64_t, int32_t, int32_t, uint16_t*,
+                                           uint16_t*, void*, void*, int, void*, hipStream_t);
+moe_status_t moe_adamw_launch(const moe::AdamwArgs*, uint32_t, int, int, int, hipStream_t);
+moe_status_t moe_adamw_advance_launch(int32_t*, const float*, hipStream_t);
+}
+
+namespace {
+
+inline uintptr_t U(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+inline bool aligned(const void* p, unsigned n) { return (U(p) & (n - 1)) == 0; }
+inline hipStream_t S(void* s) { return reinterpret_cast<hipStream_t>(s); }
+inline bool is_float_type(int32_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_F32; }
+inline unsigned width(int32_t t) { return t == MOE_OUT_F32 ? 4 : 2; }
+
+constexpr int32_t kNormMaxD = 32768;
+
+// rows of d elements of `bytes` each at this pitch move in 16-byte pieces
+inline bool whole_pieces(const void* p, int64_t ld, unsigned bytes) { return aligned(p, 16) && (ld * bytes) % 16 == 0; }
+
+// sizes of the gated block (d, f multiples of 8; the weight's byte offsets in 32 bits)
+inline moe_status_t ffn_sizes(int64_t T, int32_t d, int32_t f) {
+  if (T < 0 || d < 1 || f < 1) return MOE_ERR_INVALID_ARG;
+  if (T > INT32_MAX || d % 8 || f % 8 || d > (1 << 20) || f > (1 << 20) || 2 * (int64_t)f * d >= ((int64_t)1 << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ldx, const void* w, int32_t w_dtype, const void* r,
+                             int32_t r_dtype, int64_t ldr, void* s, int64_t lds, int64_t T, int32_t d, float eps,
+                             uint16_t* y, uint8_t* q, uint8_t* q_scale, float* rstd, void* stream) {
+  if (T < 0 || d < 1 || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (T > INT32_MAX || d > kNormMaxD || (q && d % 32)) return MOE_ERR_UNSUPPORTED;
+  if (!is_float_type(w_dtype) || (r && !is_float_type(r_dtype))) return MOE_ERR_UNSUPPORTED;
+  if (!q != !q_scale || !r != !s) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || (!y && !q)) return MOE_ERR_INVALID_ARG;
+  if (ldx < d || (r && (ldr < d || lds < d))) return MOE_ERR_INVALID_ARG;
+  const unsigned rb = width(r_dtype);
+  if (!aligned(x, 2) || !aligned(w, width(w_dtype)) || !aligned(y, 2) || !aligned(rstd, 4) ||
+      (r && (!aligned(r, rb) || !aligned(s, rb))))
+    return MOE_ERR_ALIGNMENT;
+  const bool vec = d % 8 == 0 && whole_pieces(x, ldx, 2) && aligned(w, 16) && aligned(y, 16) && aligned(q, 8) &&
+                   (!r || (whole_pieces(r, ldr, rb) && whole_pieces(s, lds, rb)));
+  if (q && !vec) return MOE_ERR_ALIGNMENT;
+  moe::NormArgs a{};
+  a.x = x;
+  a.r = r;
+  a.w = w;
+  a.s = s;
+  a.y = y;
+  a.q = q;
+  a.qs = q_scale;
+  a.rstd = rstd;
+  a.T = T;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.lds = lds;
+  a.d = d;
+  a.w_f32 = w_dtype == MOE_OUT_F32;
+  a.eps = eps;
+  return moe_add_rmsnorm_launch(&a, !r ? moe::RES_NONE : r_dtype == MOE_OUT_F32 ? moe::RES_F32 : moe::RES_BF16, vec,
+                                S(stream));
+}
+
+size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d) {
+  if (T < 0 || T > INT32_MAX || d < 1 || d > kNormMaxD) return 0;
+  const size_t n = (size_t)moe_norm_backward_parts(T) * (size_t)d * 4;
+  return n < 256 ? 256 : n;
+}
+
+moe_status_t moe_add_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const void* s, int32_t s_dtype, int64_t lds,
+                                      const void* w, int32_t w_dtype, const float* rstd, const void* dres,
+                                      int64_t lddres, int64_t T, int32_t d, uint16_t* dx, float* ds, float* dw,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || d < 1 || !dw) return MOE_ERR_INVALID_ARG;
+  if (T > INT32_MAX || d > kNormMaxD || !is_float_type(w_dtype) || !is_float_type(s_dtype)) return MOE_ERR_UNSUPPORTED;
+  if ((s_dtype == MOE_OUT_F32) != (ds != nullptr) && T > 0) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dy || !s || !w || !rstd || !dx)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (lddy < d || lds < d || (dres && lddres < d))) return MOE_ERR_INVALID_ARG;
+  const unsigned sb = width(s_dtype);
+  if (!aligned(dw, 4)) return MOE_ERR_ALIGNMENT;
+  if (T > 0 && (!aligned(dy, 2) || !aligned(s, sb) || !aligned(w, width(w_dtype)) || !aligned(rstd, 4) ||
+                !aligned(dres, sb) || !aligned(dx, 2) || !aligned(ds, 4)))
+    return MOE_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < moe_add_rmsnorm_backward_workspace_bytes(T, d)) return MOE_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MOE_ERR_ALIGNMENT;
+  const bool vec = d % 8 == 0 && whole_pieces(dy, lddy, 2) && whole_pieces(s, lds, sb) && aligned(w, 16) &&
+                   (!dres || whole_pieces(dres, lddres, sb)) && aligned(dx, 16) && aligned(ds, 16);
+  moe::NormBwdArgs a{};
+  a.dy = dy;
+  a.s = s;
+  a.w = w;
+  a.rstd = rstd;
+  a.dres = dres;
+  a.dx = dx;
+  a.ds = ds;
+  a.part = reinterpret_cast<float*>(ws);
+  a.T = T;
+  a.lddy = lddy;
+  a.lds = lds;
+  a.lddres = lddres;
+  a.d = d;
+  a.w_f32 = w_dtype == MOE_OUT_F32;
+  return moe_rmsnorm_backward_launch(&a, s_dtype == MOE_OUT_F32, vec, dw, S(stream));
+}
+
+size_t moe_gated_ffn_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t keep_h, int32_t strided_x) {
+  if (ffn_sizes(T, d, f) != MOE_OK) return 0;
+  return moe_gated_ffn_ws_impl(T, d, f, keep_h != 0, strided_x != 0);
+}
+
+moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, const uint16_t* w2,
+                           const uint16_t* res, int64_t ldres, int64_t T, int32_t d, int32_t f, uint16_t* h,
+                           uint16_t* gu, uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status_t st = ffn_sizes(T, d, f);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!x || !w1p || !w2 || !y || (gu && !h) || y == x) return MOE_ERR_INVALID_ARG;
+  if (ldx < d || (res && ldres < d) || (res == y && res && ldres != d)) return MOE_ERR_INVALID_ARG;
+  if (ldx % 8 || (res && ldres % 8)) return MOE_ERR_ALIGNMENT;
+  if (!aligned(x, 16) || !aligned(w1p, 16) || !aligned(w2, 16) || !aligned(res, 16) || !aligned(h, 16) ||
+      !aligned(gu, 16) || !aligned(y, 16))
+    return MOE_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < moe_gated_ffn_ws_impl(T, d, f, h != nullptr, ldx != d)) return MOE_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MOE_ERR_ALIGNMENT;
+  return moe_gated_ffn_launch(x, ldx, w1p, w2, res, ldres, T, d, f, h, gu, y, ws, S(stream));
+}
+
+size_t moe_gated_ffn_backward_workspace_bytes(void) { return moe_gated_ffn_backward_ws_impl(); }
+
+moe_status_t moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* gu, const uint16_t* h,
+                                    const uint16_t* w1p, const uint16_t* w2, int64_t T, int32_t d, int32_t f,
+                                    int32_t out_dtype, uint16_t* dgu, uint16_t* dx, void* dw1p, void* dw2, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  const moe_status_t st = ffn_sizes(T, d, f);
+  if (st != MOE_OK) return st;
+  if (d % 64 || f % 32 || !is_float_type(out_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (!dw1p || !dw2) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dy || !x || !gu || !h || !w1p || !w2 || !dgu || !dx)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(gu, 16) || !aligned(h, 16) || !aligned(w1p, 16) ||
+      !aligned(w2, 16) || !aligned(dgu, 16) || !aligned(dx, 16) || !aligned(dw1p, 16) || !aligned(dw2, 16))
+    return MOE_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < moe_gated_ffn_backward_ws_impl()) return MOE_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return MOE_ERR_ALIGNMENT;
+  return moe_gated_ffn_backward_launch(dy, x, gu, h, w1p, w2, T, d, f, dgu, dx, dw1p, dw2, out_dtype == MOE_OUT_F32, ws,
+                                       S(stream));
+}
+
+moe_status_t moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_config* c, int32_t* step,
+                            const float* grad_scale, void* stream) {
+  if (count < 0 || !c || !step || (count > 0 && !tensors)) return MOE_ERR_INVALID_ARG;
+  if (!(c->beta1 >= 0 && c->beta1 < 1 && c->beta2 >= 0 && c->beta2 < 1 && c->eps >= 0) || !std::isfinite(c->lr) ||
+      !std::isfinite(c->weight_decay) || !std::isfinite(c->eps))
+    return MOE_ERR_INVALID_ARG;
+  if ((c->state_bits != 32 && c->state_bits != 8) || !is_float_type(c->param_dtype) || !is_float_type(c->grad_dtype))
+    return MOE_ERR_UNSUPPORTED;
+  if (!aligned(step, 4) || !aligned(grad_scale, 4)) return MOE_ERR_ALIGNMENT;
+  const bool s8 = c->state_bits == 8;
+  bool master = false, seen = false;
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return MOE_ERR_INVALID_ARG;
+    if (t.n >= ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return MOE_ERR_INVALID_ARG;
+    if (s8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return MOE_ERR_INVALID_ARG;
+    if (seen && master != (t.master != nullptr)) return MOE_ERR_INVALID_ARG;
+    master = t.master != nullptr;
+    seen = true;
+    if (master && c->param_dtype == MOE_OUT_F32) return MOE_ERR_INVALID_ARG;
+    if (!aligned(t.param, width(c->param_dtype)) || !aligned(t.grad, width(c->grad_dtype)) || !aligned(t.master, 4) ||
+        (!s8 && (!aligned(t.exp_avg, 4) || !aligned(t.exp_avg_sq, 4))))
+      return MOE_ERR_ALIGNMENT;
+  }
+  moe::AdamwArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.step = step;
+  a.gscale = grad_scale;
+  a.log_b1 = std::log(c->beta1);
+  a.log_b2 = std::log(c->beta2);
+  a.lr = (float)c->lr;
+  a.b1 = (float)c->beta1;
+  a.b2 = (float)c->beta2;
+  a.omb1 = (float)(1.0 - c->beta1);
+  a.omb2 = (float)(1.0 - c->beta2);
+  a.eps = (float)c->eps;
+  a.wd = (float)c->weight_decay;
+  a.seed = c->seed;
+  const int pm = master ? 0 : c->param_dtype == MOE_OUT_F32 ? 2 : 1;
+  // launches of up to kAdamwTensors tensors and about 2^30 workgroups
+  int32_t i = 0;
+  while (i < count) {
+    int k = 0;
+    int64_t chunks = 0;
+    a.first = i;
+    while (i < count && k < moe::kAdamwTensors) {
+      const moe_adamw_tensor& t = tensors[i];
+      const int64_t n = (t.n + moe::kAdamwChunk - 1) / moe::kAdamwChunk;
+      if (k > 0 && chunks + n > ((int64_t)1 << 30)) break;
+      a.t[k] = moe::AdamwTensor{t.param, t.master, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,
+                                t.exp_avg_sq_scale, t.n};
+      a.start[k] = (uint32_t)chunks;
+      chunks += n;
+      ++k;
+      ++i;
+    }
+    a.start[k] = (uint32_t)chunks;
+    a.count = k;
+    if (chunks == 0) continue;
+    const moe_status_t st =
+        moe_adamw_launch(&a, (uint32_t)chunks, s8, pm, c->grad_dtype == MOE_OUT_F32, S(stream));
+    if (st != MOE_OK) return st;
+  }
+  return moe_adamw_advance_launch(step, grad_scale, S(stream));
+}
+
+}  // extern "C"

@@ -58,6 +58,10 @@ enum { BL_NK = 0, BL_PACKED = 1, BL_KN = 2 };
 // kernel-internal epilogue: SwiGLU that also stores the pre-activations
 // (C_aux != NULL); its own instantiation keeps the h-only SwiGLU kernel lean
 constexpr int EPI_SWIGLU_AUX = 7;
+// kernel-internal epilogue: C = bf16(residual + A Bop), the residual bf16
+// rows in C_aux (pitch ld_aux) loaded into the accumulators, so that the sum
+// is rounded once
+constexpr int EPI_RESIDUAL = 8;
 static_assert(EPI_SWIGLU_AUX != MOE_EPI_NONE && EPI_SWIGLU_AUX != MOE_EPI_SWIGLU &&
                   EPI_SWIGLU_AUX != MOE_EPI_SWIGLU_MXFP8 && EPI_SWIGLU_AUX != MOE_EPI_SWIGLU_BWD,
               "a kernel-internal epilogue value");
@@ -534,6 +538,26 @@ __global__ void __launch_bounds__(THREADS, 1) gg_fwd_kernel(GGArgs a) {
       if (nk > 1) issue(b1, 1);
       if (nk > 2) issue(b2, 2);
       if (nk > 3) issue(b3, 3);
+      if constexpr (EPI == EPI_RESIDUAL) {
+        // in flight together with the first stages
+        {
+          const int lane = threadIdx.x & 63;
+          const uint16_t* const res = reinterpret_cast<const uint16_t*>(a.Caux) + m0 * a.ld_aux;
+#pragma unroll
+          for (int j = 0; j < ACT; ++j) {
+            const int mr = xrow0 + j * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+              const int n = n0 + wn_ * WTN + i * 16 + 4 * (lane >> 4);
+              if (mr < rows && n < a.N) {
+                const uint2 v = *reinterpret_cast<const uint2*>(res + mr * a.ld_aux + n);
+                acc[i][j] = f32x4_t{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                                    __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u)};
+              }
+            }
+          }
+        }
+      }
       sync(-1);                 // stage 0 landed
       if (second) sync(-1);     // the half-step offset
       int s = 0;
@@ -903,6 +927,18 @@ moe_status_t launch_fwd(const GGArgs& a, int epilogue, int out_f32, int b_layout
   } else {
     hipLaunchKernelGGL((gg_fwd_kernel<MOE_EPI_NONE, MOE_OUT_BF16, BL_NK>), g, t, 0, s, b);
   }
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+// bf16, one dense product with the residual in its accumulators (B [1, N, K],
+// C_aux = the residual, pitch ld_aux)
+moe_status_t launch_fwd_residual(const GGArgs& a, hipStream_t s) {
+  using namespace fwd;
+  GGArgs b = a;
+  b.n_tiles = (a.N + BN - 1) / BN;
+  const int64_t max_tiles = ((a.m_cap + BM - 1) / BM + a.G) * b.n_tiles;
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(moe_host::device_cu_count(), max_tiles));
+  hipLaunchKernelGGL((gg_fwd_kernel<EPI_RESIDUAL, MOE_OUT_BF16, BL_NK>), dim3((unsigned)grid), dim3(THREADS), 0, s, b);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -26,6 +26,7 @@ struct GGArgs {
   uint32_t sched_epoch;    // the launch's epoch (tile_queue.h)
   uint32_t sched_next;     // the epoch of the slot's next launch
   float* part;             // ragged-M bf16: workspace of the split tail's partial sums, or NULL
+  int64_t ld_aux;          // row pitch of the residual in Caux (launch_fwd_residual only)
 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;

@@ -39,6 +39,9 @@ EXPORTS = (
     "moe_pack_weights",
     "moe_pack_weights_mxfp8_bytes", "moe_pack_weights_mxfp8",
     "moe_route_fused_workspace_bytes", "moe_route_fused", "moe_permute_routed", "mxfp4_quantize",
+    "moe_add_rmsnorm", "moe_add_rmsnorm_backward_workspace_bytes", "moe_add_rmsnorm_backward",
+    "moe_gated_ffn_workspace_bytes", "moe_gated_ffn", "moe_gated_ffn_backward_workspace_bytes", "moe_gated_ffn_backward",
+    "moe_adamw_step",
     # measurement only (include/moe_bench.h)
     "moe_bench_mfma_flops", "moe_bench_mfma_ceiling",
 )
@@ -96,6 +99,16 @@ def load_library(path: str = LIB_PATH, require_gpu: bool = True):
             "moe_route_fused": (ctypes.c_int, [P, P, P, i64, i32, i32, i32, i32, P, P, P, P, sz, P, P]),
             "moe_permute_routed": (ctypes.c_int, [P, P, i64, i32, i32, i32, P, P, P, P, P, P, sz, P, P]),
             "mxfp4_quantize": (ctypes.c_int, [P, i64, i32, P, P, P]),
+            "moe_add_rmsnorm": (ctypes.c_int, [P, i64, P, i32, P, i32, i64, P, i64, i64, i32, ctypes.c_float, P, P, P, P,
+                                               P]),
+            "moe_add_rmsnorm_backward_workspace_bytes": (sz, [i64, i32]),
+            "moe_add_rmsnorm_backward": (ctypes.c_int, [P, i64, P, i32, i64, P, i32, P, P, i64, i64, i32, P, P, P, P, sz,
+                                                        P]),
+            "moe_gated_ffn_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
+            "moe_gated_ffn": (ctypes.c_int, [P, i64, P, P, P, i64, i64, i32, i32, P, P, P, P, sz, P]),
+            "moe_gated_ffn_backward_workspace_bytes": (sz, []),
+            "moe_gated_ffn_backward": (ctypes.c_int, [P, P, P, P, P, P, i64, i32, i32, i32, P, P, P, P, P, sz, P]),
+            "moe_adamw_step": (ctypes.c_int, [P, i32, P, P, P, P]),
             "moe_bench_mfma_flops": (i64, [i64, i32]),
             "moe_bench_mfma_ceiling": (ctypes.c_int, [i32, i32, P, i64, P]),
         }
@@ -659,6 +672,268 @@ def swiglu_backward_mxfp8(gu: torch.Tensor, dh: torch.Tensor, group_sizes: torch
                                            _ptr(sT), _ptr(q), _ptr(sc), _ptr(flag), _stream(dev)),
            "moe_swiglu_backward_mxfp8")
     return qT, sT, q, sc
+
+
+# ------------------------------------------------------------------ dense operators around the layer
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise MoeError(what)
+
+
+def _rows(t: torch.Tensor, what: str) -> int:
+    """The row pitch of a 2-D GPU tensor whose rows are contiguous."""
+    _need(t.is_cuda and t.dim() == 2, f"{what}: a 2-D tensor on the GPU")
+    T, d = t.shape
+    st = t.stride()
+    _need(T == 0 or d <= 1 or st[1] == 1, f"{what}: the elements of a row must be contiguous")
+    if T <= 1:
+        return d
+    _need(st[0] >= d, f"{what}: rows must not overlap")
+    return st[0]
+
+
+def _float_code(t: torch.Tensor, what: str) -> int:
+    _need(t.dtype in (torch.bfloat16, torch.float32), f"{what}: bf16 or fp32")
+    return MOE_OUT_F32 if t.dtype == torch.float32 else MOE_OUT_BF16
+
+
+def _invoke(dev: torch.device, what: str, *args) -> None:
+    """The library call `what` with the tensors' device current and its
+    current stream as the last argument."""
+    fn = getattr(lib(), what)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev)), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)), what)
+
+
+def _same_device(dev: torch.device, *ts) -> None:
+    for t in ts:
+        _need(t is None or t.device == dev, "tensors must be on one GPU")
+
+
+def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+                bf16: bool = True, mxfp8: bool = False, keep_rstd: bool = False,
+                out_s: Optional[torch.Tensor] = None):
+    """Root-mean-square norm behind the residual's addition: s = x + residual
+    (rounded to the residual's type; x itself without one), y = s / sqrt(mean(s^2)
+    + eps) * weight.  x bf16 [T, d] and residual bf16 or fp32 [T, d] may have a
+    row pitch; weight bf16 or fp32 [d].  -> dict(y bf16 [T, d] (bf16=True), q
+    uint8 [T, d] and scale uint8 [T, d/32] (mxfp8=True: as mxfp8_quantize(y,
+    0)), s, rstd fp32 [T] (keep_rstd=True)), None where not asked for.
+    out_s: where s goes (residual itself: updated in place)."""
+    ldx = _rows(x, "x")
+    _need(x.dtype == torch.bfloat16, "x: bf16")
+    _need(bf16 or mxfp8, "add_rmsnorm: no output asked for")
+    T, d = x.shape
+    dev = x.device
+    _same_device(dev, weight, residual, out_s)
+    _need(weight.shape == (d,) and weight.is_contiguous(), "weight: [d], contiguous")
+    r_code = ldr = lds = 0
+    s = x
+    if residual is not None:
+        ldr = _rows(residual, "residual")
+        _need(residual.shape == x.shape, "residual: the shape of x")
+        r_code = _float_code(residual, "residual")
+        if out_s is None:
+            s, lds = torch.empty((T, d), dtype=residual.dtype, device=dev), d
+        else:
+            lds = _rows(out_s, "out_s")
+            _need(out_s.shape == x.shape and out_s.dtype == residual.dtype, "out_s: shape and type of the residual")
+            s = out_s
+    else:
+        _need(out_s is None, "out_s without a residual: s is x itself")
+    y = torch.empty((T, d), dtype=torch.bfloat16, device=dev) if bf16 else None
+    q = sc = None
+    if mxfp8:
+        q = torch.empty((T, d), dtype=torch.uint8, device=dev)
+        sc = torch.empty((T, d // 32), dtype=torch.uint8, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if keep_rstd else None
+    _invoke(dev, "moe_add_rmsnorm", _ptr(x), ldx, _ptr(weight), _float_code(weight, "weight"), _ptr(residual), r_code,
+            ldr, None if residual is None else _ptr(s), lds, T, d, eps, _ptr(y), _ptr(q), _ptr(sc), _ptr(rstd))
+    return dict(y=y, q=q, scale=sc, s=s, rstd=rstd)
+
+
+def add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *,
+                         dresidual: Optional[torch.Tensor] = None):
+    """Backward of add_rmsnorm from its s and rstd: dy bf16 [T, d] is y's
+    gradient, dresidual (of s's type) what reaches s along the residual
+    stream.  -> dict(dx bf16 [T, d], ds: the same gradient in s's type (dx
+    itself where s is bf16), dweight fp32 [d]): ds is the gradient of both x
+    and the residual."""
+    lddy, lds = _rows(dy, "dy"), _rows(s, "s")
+    T, d = dy.shape
+    dev = dy.device
+    _same_device(dev, s, weight, rstd, dresidual)
+    _need(dy.dtype == torch.bfloat16 and s.shape == dy.shape, "dy: bf16, of the shape of s")
+    _need(weight.shape == (d,) and weight.is_contiguous(), "weight: [d], contiguous")
+    _need(rstd.shape == (T,) and rstd.dtype == torch.float32 and rstd.is_contiguous(), "rstd: fp32 [T]")
+    ldr = 0
+    if dresidual is not None:
+        ldr = _rows(dresidual, "dresidual")
+        _need(dresidual.shape == s.shape and dresidual.dtype == s.dtype, "dresidual: shape and type of s")
+    code = _float_code(s, "s")
+    dx = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+    ds = torch.empty((T, d), dtype=torch.float32, device=dev) if code == MOE_OUT_F32 else None
+    dw = torch.empty(d, dtype=torch.float32, device=dev)
+    need = lib().moe_add_rmsnorm_backward_workspace_bytes(T, d)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _invoke(dev, "moe_add_rmsnorm_backward", _ptr(dy), lddy, _ptr(s), code, lds, _ptr(weight),
+            _float_code(weight, "weight"), _ptr(rstd), _ptr(dresidual), ldr, T, d, _ptr(dx), _ptr(ds), _ptr(dw),
+            _ptr(ws), need)
+    return dict(dx=dx, ds=dx if ds is None else ds, dweight=dw)
+
+
+def _ffn_weights(w1p: torch.Tensor, w2: torch.Tensor, d: int, dev: torch.device) -> int:
+    _same_device(dev, w1p, w2)
+    _need(w1p.dtype == torch.bfloat16 and w2.dtype == torch.bfloat16, "w1p, w2: bf16")
+    _need(w1p.is_contiguous() and w2.is_contiguous(), "w1p, w2: contiguous")
+    f = w2.shape[-1]
+    _need(w2.shape == (d, f) and w1p.shape == (2 * f, d), "w1p: [2f, d], w2: [d, f]")
+    return f
+
+
+def gated_ffn(x: torch.Tensor, w1p: torch.Tensor, w2: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+              keep: bool = False, out: Optional[torch.Tensor] = None):
+    """The gated feed-forward block on one weight set (a shared expert):
+    y = residual + (silu(x Wg^T) * (x Wu^T)) w2^T, w1p = [Wg; Wu] bf16 [2f, d],
+    w2 bf16 [d, f], x bf16 [T, d] and residual bf16 [T, d] (row pitches that
+    are multiples of 8).  Any T, a single token included.  -> y bf16 [T, d]; with
+    keep, (y, dict(h bf16 [T, f], gu bf16 [T, 2f])) for gated_ffn_backward.
+    out: where y goes (may be residual)."""
+    ldx = _rows(x, "x")
+    _need(x.dtype == torch.bfloat16, "x: bf16")
+    T, d = x.shape
+    dev = x.device
+    f = _ffn_weights(w1p, w2, d, dev)
+    ldr = 0
+    if residual is not None:
+        _same_device(dev, residual)
+        ldr = _rows(residual, "residual")
+        _need(residual.dtype == torch.bfloat16 and residual.shape == x.shape, "residual: bf16, the shape of x")
+    if out is None:
+        out = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _same_device(dev, out)
+        _need(out.shape == (T, d) and out.dtype == torch.bfloat16 and out.is_contiguous(), "out: bf16 [T, d], contiguous")
+    h = gu = None
+    if keep:
+        h = torch.empty((T, f), dtype=torch.bfloat16, device=dev)
+        gu = torch.empty((T, 2 * f), dtype=torch.bfloat16, device=dev)
+    need = lib().moe_gated_ffn_workspace_bytes(T, d, f, int(keep), int(ldx != d))
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _invoke(dev, "moe_gated_ffn", _ptr(x), ldx, _ptr(w1p), _ptr(w2), _ptr(residual), ldr, T, d, f, _ptr(h), _ptr(gu),
+            _ptr(out), _ptr(ws), need)
+    return (out, dict(h=h, gu=gu)) if keep else out
+
+
+def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, saved: dict, w1p: torch.Tensor, w2: torch.Tensor, *,
+                       out_dtype: torch.dtype = torch.bfloat16):
+    """Backward of gated_ffn from what it kept (the residual's gradient is dy
+    itself, not added to dx).  dy, x bf16 [T, d] -> dict(dx bf16 [T, d], dw1p
+    [2f, d], dw2 [d, f] in out_dtype (bf16 or fp32), dgu bf16 [T, 2f])."""
+    dev = _dev(dy, x, saved["gu"], saved["h"], w1p, w2)
+    _same_device(dev, x, saved["gu"], saved["h"])
+    _need(dy.dim() == 2, "dy: [T, d]")
+    T, d = dy.shape
+    f = _ffn_weights(w1p, w2, d, dev)
+    _need(all(t.dtype == torch.bfloat16 for t in (dy, x, saved["gu"], saved["h"])), "dy, x, gu, h: bf16")
+    _need(x.shape == (T, d) and saved["gu"].shape == (T, 2 * f) and saved["h"].shape == (T, f),
+          "x: [T, d], gu: [T, 2f], h: [T, f]")
+    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype: bf16 or fp32")
+    dgu = torch.empty((T, 2 * f), dtype=torch.bfloat16, device=dev)
+    dx = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+    dw1p = torch.empty((2 * f, d), dtype=out_dtype, device=dev)
+    dw2 = torch.empty((d, f), dtype=out_dtype, device=dev)
+    need = lib().moe_gated_ffn_backward_workspace_bytes()
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _invoke(dev, "moe_gated_ffn_backward", _ptr(dy), _ptr(x), _ptr(saved["gu"]), _ptr(saved["h"]), _ptr(w1p), _ptr(w2),
+            T, d, f, MOE_OUT_F32 if out_dtype == torch.float32 else MOE_OUT_BF16, _ptr(dgu), _ptr(dx), _ptr(dw1p),
+            _ptr(dw2), _ptr(ws), need)
+    return dict(dx=dx, dw1p=dw1p, dw2=dw2, dgu=dgu)
+
+
+class AdamwConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("state_bits", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("seed", ctypes.c_uint32)]
+
+
+_CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+_SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def adamw_state(params, bits: int = 32):
+    """The optimiser's state before the first step, for adamw_step: dict of
+    lists exp_avg, exp_avg_sq (fp32, or with bits = 8 E4M3 codes, and then
+    exp_avg_scale, exp_avg_sq_scale, else None) and step (int32 [1], 0)."""
+    _need(bits in (8, 32), "bits: 8 or 32")
+    _need(len(params) > 0, "params: at least one tensor")
+    dt = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    zeros = lambda n, t, p: torch.zeros(n, dtype=torch.uint8 if t in _SCALE_TYPES or t in _CODE_TYPES else t,  # noqa: E731
+                                        device=p.device).view(t)
+    st = dict(exp_avg=[zeros(tuple(p.shape), dt, p) for p in params],
+              exp_avg_sq=[zeros(tuple(p.shape), dt, p) for p in params], exp_avg_scale=None, exp_avg_sq_scale=None,
+              step=torch.zeros(1, dtype=torch.int32, device=params[0].device))
+    if bits == 8:
+        for k in ("exp_avg_scale", "exp_avg_sq_scale"):
+            st[k] = [zeros((p.numel() + 31) // 32, torch.float8_e8m0fnu, p) for p in params]
+    return st
+
+
+def adamw_step(params, grads, exp_avg, exp_avg_sq, step: torch.Tensor, *, lr: float, betas=(0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 0.01, masters=None, exp_avg_scale=None, exp_avg_sq_scale=None,
+               grad_scale: Optional[torch.Tensor] = None, seed: int = 0) -> None:
+    """One AdamW step on lists of tensors, in place (adamw_state makes the
+    first state).  params bf16 or fp32 (all of one type), grads bf16 or fp32;
+    masters: fp32 copies the step works on, params then receive them rounded.
+    exp_avg, exp_avg_sq: fp32 m and v, or E4M3 codes of m and sqrt(v) with
+    E8M0 scales of 32 elements in exp_avg_scale, exp_avg_sq_scale; bf16 params
+    without masters and 8-bit states are rounded at random by a hash of (seed,
+    step, tensor, element).  step: int32 [1] on the GPU, advanced by one.
+    grad_scale: fp32 [1] on the GPU; infinite or NaN: the step is skipped."""
+    n = len(params)
+    _need(step.is_cuda and step.dtype == torch.int32 and step.numel() == 1, "step: int32 [1] on the GPU")
+    dev = step.device
+    if grad_scale is not None:
+        _need(grad_scale.device == dev and grad_scale.dtype == torch.float32 and grad_scale.numel() == 1,
+              "grad_scale: fp32 [1] on the GPU")
+    bits8 = exp_avg_scale is not None
+    _need(bits8 == (exp_avg_sq_scale is not None), "exp_avg_scale and exp_avg_sq_scale: both or neither")
+    pt = params[0].dtype if n else torch.bfloat16
+    gt = grads[0].dtype if n else torch.bfloat16
+    _need(pt in (torch.bfloat16, torch.float32) and gt in (torch.bfloat16, torch.float32), "params, grads: bf16 or fp32")
+    _need(masters is None or pt == torch.bfloat16, "masters: with bf16 params")
+    f32 = (torch.float32,)
+    st = _CODE_TYPES if bits8 else f32
+    # in the order of moe_adamw_tensor's fields
+    lists = [(params, (pt,), "params"), (masters, f32, "masters"), (grads, (gt,), "grads"), (exp_avg, st, "exp_avg"),
+             (exp_avg_sq, st, "exp_avg_sq"), (exp_avg_scale, _SCALE_TYPES, "exp_avg_scale"),
+             (exp_avg_sq_scale, _SCALE_TYPES, "exp_avg_sq_scale")]
+    numels = [p.numel() for p in params]
+    table = [None] * (8 * n)
+    table[7::8] = numels
+    written = []
+    for k, (ts, types, what) in enumerate(lists):
+        if ts is None:
+            table[k::8] = [0] * n
+            continue
+        _need(len(ts) == n, f"{what}: one tensor for each of params")
+        for i, t in enumerate(ts):
+            want = numels[i] if k < 5 else (numels[i] + 31) // 32
+            if t.dtype not in types or t.numel() != want or t.device != dev or not t.is_contiguous():
+                raise MoeError(f"{what}[{i}]: contiguous, on the GPU of step, of the type and size that go with params[{i}]")
+        ptrs = [t.data_ptr() for t in ts]
+        table[k::8] = ptrs
+        if k != 2:
+            written += [a for a, m in zip(ptrs, numels) if m]
+    _need(len(set(written)) == len(written), "adamw_step: the same tensor twice")
+    c = AdamwConfig(lr, betas[0], betas[1], eps, weight_decay, 8 if bits8 else 32,
+                    MOE_OUT_F32 if pt == torch.float32 else MOE_OUT_BF16,
+                    MOE_OUT_F32 if gt == torch.float32 else MOE_OUT_BF16, seed & 0xFFFFFFFF)
+    _invoke(dev, "moe_adamw_step", (ctypes.c_int64 * (8 * n))(*table), n, ctypes.byref(c), _ptr(step), _ptr(grad_scale))
 
 
 # ------------------------------------------------------------------ measurement only

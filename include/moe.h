@@ -480,6 +480,146 @@ moe_status_t moe_swiglu_backward_mxfp8(const uint16_t* gu, const uint16_t* dh, i
                                        uint8_t* scaleT, uint8_t* q_rows, uint8_t* scale_rows, uint32_t* err_flag,
                                        void* stream);
 
+/* ========================================================================
+ * Dense operators around the expert layer: what a transformer block needs
+ * next to it to be trained or served (the norm in front of the layer, a
+ * shared expert beside the routed ones, the optimiser step on the weights).
+ * The conventions at the top of this file hold; rows may have a pitch (ld,
+ * in elements) where one is named.
+ * ======================================================================== */
+
+/* Root-mean-square norm with the residual's addition before it and MXFP8
+ * quantisation behind it.  Per row:
+ *   s = x + r                  (r NULL: s = x), rounded to r's type
+ *   rstd = 1 / sqrt(mean(s^2) + eps)
+ *   y = bf16(s * rstd * w)     and / or MXFP8 of that y
+ * The norm is that of s as it is stored.  Sums and rstd are fp32.
+ *   x [T, d] bf16, pitch ldx;  w [d] bf16 or fp32 (w_dtype MOE_OUT_BF16 /
+ *   MOE_OUT_F32);  r [T, d] bf16 or fp32 (r_dtype), pitch ldr, or NULL;
+ *   s [T, d] in r's type, pitch lds: required with r (may be r itself: the
+ *   residual stream updated in place), NULL without;
+ *   y [T, d] bf16 or NULL;  q uint8 [T, d] with q_scale uint8 [T, d/32], both
+ *   or neither: bit for bit mxfp8_group_quantize (axis 0) of y, written
+ *   whether or not y is; y and q may not both be NULL;
+ *   rstd fp32 [T] or NULL (the backward reads it).
+ * Limits: 1 <= d <= 32768 (with q: d % 32 == 0), pitches >= d, T < 2^31.
+ * With d % 8 == 0 and 16-byte aligned rows a row moves in 16-byte pieces; any
+ * other d, pitch or (2-byte, fp32: 4-byte) alignment is taken too, slower;
+ * q needs the former (else MOE_ERR_ALIGNMENT). */
+moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ldx, const void* w, int32_t w_dtype, const void* r,
+                             int32_t r_dtype, int64_t ldr, void* s, int64_t lds, int64_t T, int32_t d, float eps,
+                             uint16_t* y, uint8_t* q, uint8_t* q_scale, float* rstd, void* stream);
+
+/* Its backward.  With xh = s * rstd and the gradient dres that reaches s along
+ * the residual stream (NULL: zero):
+ *   ds = dres + rstd * (w * dy - xh * mean(w * dy * xh))
+ *   dw[j] = sum over the rows of dy[:, j] * xh[:, j]              (fp32)
+ * ds is the gradient of both x and r: dx receives it in bf16, and where s is
+ * fp32 (s_dtype), ds in fp32 too.  dres is of s's type.
+ *   dy bf16 [T, d] (pitch lddy), s [T, d] (pitch lds), dres (pitch lddres);
+ *   dx bf16 [T, d]; ds fp32 [T, d] (required iff s is fp32, else NULL);
+ *   dw fp32 [d].  dx may be dy (of pitch d) itself.
+ *   ws: moe_add_rmsnorm_backward_workspace_bytes(T, d), 256-byte aligned.
+ * T = 0 gives dw = 0.  The column sums are added in a fixed order: bitwise
+ * reproducible.  Limits and alignment as above. */
+size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d);
+moe_status_t moe_add_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const void* s, int32_t s_dtype, int64_t lds,
+                                      const void* w, int32_t w_dtype, const float* rstd, const void* dres,
+                                      int64_t lddres, int64_t T, int32_t d, uint16_t* dx, float* ds, float* dw,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/* Gated feed-forward block on one weight set (a shared expert):
+ *   g = x Wg^T, u = x Wu^T, h = bf16(silu(g) * u), y = bf16(res + h W2^T)
+ * with w1p bf16 [2f, d] (rows [0, f) gate, [f, 2f) up) and w2 bf16 [d, f], as
+ * one expert of the grouped form; accumulation fp32, the residual added
+ * before y's one rounding.
+ *   x bf16 [T, d], pitch ldx (a multiple of 8; other than d it never takes the
+ *   many-token kernels);  res bf16 [T, d], pitch ldres (a multiple of 8), or
+ *   NULL;  y bf16 [T, d] (may be res, of pitch d; not x);
+ *   h bf16 [T, f] or NULL (kept in ws);  gu bf16 [T, 2f] or NULL: the
+ *   pre-activations [g | u], which the backward reads (needs h).
+ *   ws: moe_gated_ffn_workspace_bytes(T, d, f, h != NULL, ldx != d),
+ *   256-byte aligned; calls in flight together must not share it.
+ * Every T >= 0 runs, a single token included (T <= 16 reads the weights once,
+ * straight into the matrix instructions' operands).  Results do not depend on
+ * thread timing.  Limits: d % 8 == 0, f % 8 == 0, 8 <= d, f <= 2^20,
+ * 2 f d < 2^31, T < 2^31; all pointers 16-byte aligned. */
+size_t moe_gated_ffn_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t keep_h, int32_t strided_x);
+moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, const uint16_t* w2,
+                           const uint16_t* res, int64_t ldres, int64_t T, int32_t d, int32_t f, uint16_t* h,
+                           uint16_t* gu, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward, from gu and h of the forward (the residual's gradient is dy
+ * itself and not added to dx):
+ *   dh = dy W2, dgu = SwiGLU's backward of (gu, dh), dx = dgu W1p,
+ *   dw1p = dgu^T x [2f, d], dw2 = dy^T h [d, f]   (out_dtype bf16 or fp32)
+ * dgu bf16 [T, 2f] is an output too.  All operands contiguous and 16-byte
+ * aligned.  ws: moe_gated_ffn_backward_workspace_bytes(), 256-byte aligned.
+ * T = 0 gives zero weight gradients.  The weight gradients take two of the 64
+ * queue slots of RAGGED_K grouped_gemm: what is said there about calls in
+ * flight and about one graph on two streams holds here.  Limits: d % 64 == 0,
+ * f % 32 == 0, else as the forward. */
+size_t moe_gated_ffn_backward_workspace_bytes(void);
+moe_status_t moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* gu, const uint16_t* h,
+                                    const uint16_t* w1p, const uint16_t* w2, int64_t T, int32_t d, int32_t f,
+                                    int32_t out_dtype, uint16_t* dgu, uint16_t* dx, void* dw1p, void* dw2, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* One AdamW step over many tensors (the weights whose gradients RAGGED_K
+ * grouped_gemm, moe_gated_ffn_backward and moe_add_rmsnorm_backward give;
+ * moe_pack_weights and the quantisers read the result).  With t = *step + 1:
+ *   g = grad * grad_scale;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+ *   p = p - lr (wd p + (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
+ * in fp32.  `tensors` is a HOST array of `count` entries, read during the
+ * call; the addresses in it are device pointers and travel as kernel
+ * arguments, so the call may be captured.
+ *   param    bf16 or fp32 (param_dtype) [n]
+ *   master   fp32 [n] copy that the step works on; param (bf16) receives it
+ *            rounded to nearest.  All entries have one or none has; with
+ *            param fp32 it is NULL.  bf16 without a master: the new value is
+ *            rounded up or down at random, in proportion to the distance
+ *            (a step is often smaller than half a bf16 step).
+ *   grad     bf16 or fp32 (grad_dtype) [n]
+ *   exp_avg, exp_avg_sq   state_bits 32: fp32 [n] m and v.  state_bits 8:
+ *            uint8 [n] E4M3 codes of m and of sqrt(v), with one E8M0 scale per
+ *            32 consecutive elements in exp_avg_scale, exp_avg_sq_scale uint8
+ *            [ceil(n / 32)]: 2^e, the smallest with amax <= 448 * 2^e (e
+ *            clamped to [-127, 127], byte e + 127; amax 0: byte 0; a NaN or
+ *            infinity: byte 255, codes 0x7F), the codes rounded at random as
+ *            above.  All-zero codes and scales are the start.
+ *   step     int32, DEVICE: steps done so far; the call adds 1
+ *   grad_scale  fp32, DEVICE, or NULL (1): e.g. a clipping factor over a loss
+ *            scale.  An infinity or NaN skips the step: nothing is written.
+ * The random bits are a hash of (seed, t, the tensor's index, the element),
+ * with mix(v) = { v = (v ^ v >> 16) * 0x7FEB352D; v = (v ^ v >> 15) *
+ * 0x846CA68B; v ^ v >> 16 } on 32 bits and key = mix(mix(mix(seed) ^ t) ^
+ * index): r = mix(lo32(i) + mix(key ^ hi32(i))); m takes its low 16 bits,
+ * sqrt(v) its high 16, a bf16 param the low 16 of mix(r + 0x9E3779B9).  16
+ * bits are added right below the kept bits and the rest is cut; for E4M3
+ * values below 2^-6 of the scale, 2^-6 is added first.  So equal calls give
+ * equal results.
+ * No two entries may overlap.  n >= 0 (0: skipped), n < 2^40; pointers
+ * aligned to their type (16 bytes: moved in 16-byte pieces). */
+typedef struct moe_adamw_tensor {
+  void* param;
+  float* master;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  uint8_t* exp_avg_scale;
+  uint8_t* exp_avg_sq_scale;
+  int64_t n;
+} moe_adamw_tensor;
+typedef struct moe_adamw_config {
+  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1 */
+  int32_t state_bits;                         /* 32 | 8 */
+  int32_t param_dtype;                        /* MOE_OUT_BF16 | MOE_OUT_F32 */
+  int32_t grad_dtype;                         /* MOE_OUT_BF16 | MOE_OUT_F32 */
+  uint32_t seed;
+} moe_adamw_config;
+moe_status_t moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_config* config,
+                            int32_t* step, const float* grad_scale, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
