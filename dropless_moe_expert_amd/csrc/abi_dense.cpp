@@ -18,7 +18,7 @@ moe_status_t moe_rmsnorm_backward_launch(const moe::NormBwdArgs*, int, int, floa
 size_t moe_gated_ffn_ws_impl(int64_t, int32_t, int32_t, int, int);
 moe_status_t moe_gated_ffn_launch(const uint16_t*, int64_t, const uint16_t*, const uint16_t*, const uint16_t*, int64_t,
                                   int64_t, int32_t, int32_t, uint16_t*, uint16_t*, uint16_t*, void*, hipStream_t);
-size_t moe_gated_ffn_backward_ws_impl(void);
+size_t moe_gated_ffn_backward_ws_impl(int64_t, int32_t, int32_t);
 moe_status_t moe_gated_ffn_backward_launch(const uint16_t*, const uint16_t*, const uint16_t*, const uint16_t*,
                                            const uint16_t*, const uint16_t*, int64_t, int32_t, int32_t, uint16_t*,
                                            uint16_t*, void*, void*, int, void*, hipStream_t);
@@ -152,7 +152,10 @@ moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, 
   return moe_gated_ffn_launch(x, ldx, w1p, w2, res, ldres, T, d, f, h, gu, y, ws, S(stream));
 }
 
-size_t moe_gated_ffn_backward_workspace_bytes(void) { return moe_gated_ffn_backward_ws_impl(); }
+size_t moe_gated_ffn_backward_workspace_bytes(int64_t T, int32_t d, int32_t f) {
+  if (ffn_sizes(T, d, f) != MOE_OK) return 0;
+  return moe_gated_ffn_backward_ws_impl(T, d, f);
+}
 
 moe_status_t moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* gu, const uint16_t* h,
                                     const uint16_t* w1p, const uint16_t* w2, int64_t T, int32_t d, int32_t f,
@@ -160,13 +163,13 @@ moe_status_t moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, const
                                     size_t ws_bytes, void* stream) {
   const moe_status_t st = ffn_sizes(T, d, f);
   if (st != MOE_OK) return st;
-  if (d % 64 || f % 32 || !is_float_type(out_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (!is_float_type(out_dtype)) return MOE_ERR_UNSUPPORTED;
   if (!dw1p || !dw2) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!dy || !x || !gu || !h || !w1p || !w2 || !dgu || !dx)) return MOE_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(gu, 16) || !aligned(h, 16) || !aligned(w1p, 16) ||
       !aligned(w2, 16) || !aligned(dgu, 16) || !aligned(dx, 16) || !aligned(dw1p, 16) || !aligned(dw2, 16))
     return MOE_ERR_ALIGNMENT;
-  if (!ws || ws_bytes < moe_gated_ffn_backward_ws_impl()) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < moe_gated_ffn_backward_ws_impl(T, d, f)) return MOE_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return MOE_ERR_ALIGNMENT;
   return moe_gated_ffn_backward_launch(dy, x, gu, h, w1p, w2, T, d, f, dgu, dx, dw1p, dw2, out_dtype == MOE_OUT_F32, ws,
                                        S(stream));

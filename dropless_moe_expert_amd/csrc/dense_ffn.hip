@@ -11,15 +11,15 @@
 //    workgroup owns 16 weight rows, its wavefronts split K and go straight
 //    from HBM to MFMA fragments, no LDS stage; the wavefronts' sums meet in
 //    LDS in a fixed order;
-//  * a moderate number: BM x BN tiles through LDS, K split over workgroups
-//    until the chip is full, the fp32 partial sums added by a second kernel
-//    in split order;
+//  * a moderate number: 64 or 128 x 128 tiles streamed through LDS, K split
+//    over workgroups until the chip is full, the fp32 partial sums added by a
+//    second kernel in split order;
 //  * many: the persistent 256 x 256 kernels of the grouped products
 //    (gg_bf16.hip) with one group.
 #include <algorithm>
 
 #include "dense_args.h"
-#include "gg_common.h"
+#include "gg_pipeline.h"
 
 namespace moe {
 moe_status_t launch_fwd(const GGArgs& a, int epilogue, int out_f32, int b_layout, hipStream_t s);  // gg_bf16.hip
@@ -29,17 +29,28 @@ size_t fwd_split_workspace_bytes();                                             
 
 namespace ffn {
 
-struct ProdArgs {
-  const uint16_t* x;     // [T, K] rows, pitch ldx
-  const uint16_t* w;     // [N, K] (plain) or [2N, K] (gated: N gate rows, N up rows)
-  const uint16_t* res;   // plain: [T, N], pitch ldr, or NULL
-  uint16_t* out;         // [T, N]
-  uint16_t* aux;         // gated: [T, 2N] pre-activations, or NULL
-  float* part;           // split: [S, T, N or 2N] partial sums
-  int64_t ldx, ldr;
-  int T, N, K;
+// The products.  C[m, n] = sum_k Q[m, k] P[n, k]; an operand is either rows
+// with K contiguous or (K-outer) rows of K with its own index contiguous.
+enum Mode {
+  GATE = 0,   // P = W1p rows (gate and up), Q = x;            h (and gu)
+  DOWN = 1,   // P = W2 rows, Q = h;                           y = residual + ...
+  DGU = 2,    // P = W2 [K = d, N = f] K-outer, Q = dy;        dgu from dh and gu
+  DX = 3,     // P = W1p [K = 2f, N = d] K-outer, Q = dgu;     dx
+  WGRAD = 4   // P = x or h [K = T, N], Q = dgu or dy [K = T, M], both K-outer
+};
+
+struct Prod {
+  const uint16_t* p;
+  const uint16_t* q;
+  const uint16_t* res;   // DOWN: residual [M, N] (pitch ldr) or NULL; DGU: gu [M, 2N]
+  uint16_t* out;         // [M, N]; DGU: [M, 2N]
+  uint16_t* aux;         // GATE: pre-activations [M, 2N] or NULL
+  float* part;           // S > 1: [S, M, N] (GATE: 2N) partial sums
+  int64_t ldp, ldq, ldr;
+  int M, N, K;
   int S;                 // splits of K
   int mtiles, ntiles;
+  int out_f32;           // WGRAD: fp32 output
 };
 
 __device__ __forceinline__ f32x4_t mfma(uint4 w, uint4 x, f32x4_t c) {
@@ -54,7 +65,7 @@ __device__ __forceinline__ f32x4_t mfma(uint4 w, uint4 x, f32x4_t c) {
 constexpr int kFewWaves = 8, kFewUnroll = 8;
 
 template <int MT, bool GATED>
-__global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(ProdArgs a) {
+__global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(Prod a) {
   constexpr int NW = kFewWaves, U = kFewUnroll;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int r16 = lane & 15, g4 = lane >> 4;
@@ -65,10 +76,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(ProdArgs a) 
   } else {
     row = min(n0 + r16, a.N - 1);
   }
-  const uint16_t* wp = a.w + (int64_t)row * a.K + 8 * g4;
+  const uint16_t* wp = a.p + (int64_t)row * a.ldp + 8 * g4;
   const uint16_t* xp[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) xp[m] = a.x + (int64_t)min(16 * m + r16, a.T - 1) * a.ldx + 8 * g4;
+  for (int m = 0; m < MT; ++m) xp[m] = a.q + (int64_t)min(16 * m + r16, a.M - 1) * a.ldq + 8 * g4;
   const int steps = (a.K + 31) / 32;
   f32x4_t acc[MT];
 #pragma unroll
@@ -115,7 +126,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(ProdArgs a) 
   constexpr int PER = GATED ? 8 : 16;   // output columns of the workgroup
   for (int i = threadIdx.x; i < MT * 16 * PER; i += NW * 64) {
     const int t = i / PER, j = i % PER;
-    if (t >= a.T || n0 + j >= a.N) continue;
+    if (t >= a.M || n0 + j >= a.N) continue;
     float v = 0.f, u = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
@@ -136,174 +147,301 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(ProdArgs a) 
 }
 
 // ------------------------------------------------------------------ tiles
-// BM tokens x BN weight rows, K staged 64 at a time through two LDS buffers:
-// the next stage's loads are in flight (in registers) while the present one
-// is multiplied.  Four wavefronts, 2 x 2.  LDS rows of 128 bytes, 16-byte
-// slots XOR-swizzled by row.  Gated: a wavefront's weight rows are BN/4 gate
-// rows followed by the matching BN/4 up rows.
-template <int BM, int BN, bool GATED>
-__global__ __launch_bounds__(256) void tile_kernel(ProdArgs a) {
-  constexpr int TM = BM / 32, TN = BN / 32;
-  constexpr int XR = BM / 32, WR = BN / 32;   // 16-byte pieces per thread and stage
-  __shared__ __align__(16) uint8_t lds[2][(BM + BN) * 128];
-  // consecutive workgroups run on different XCDs; the m-tiles of one weight
-  // tile follow each other on one XCD, so its L2 reads the weights once
-  const int xcd = blockIdx.x & 7, q = blockIdx.x >> 3;
-  const int mt = q % a.mtiles, unit = (q / a.mtiles) * 8 + xcd;
+// One BM x 128 tile (m x n) of a product, over one range of K.  K is staged
+// 32 at a time in a ring of LDS buffers filled by direct-to-LDS loads, RING - 1
+// stages ahead of the stage being multiplied: the weights stream from HBM, and
+// what is in flight bounds their rate (two workgroups a compute unit).  Four
+// wavefronts, 2 (m) x 2 (n).  An operand with K contiguous is 64-byte rows,
+// 16-byte slots swizzled by row; a K-outer one is 32 rows of 256 bytes whose
+// fragments come through the LDS transpose read (gg_pipeline.h has both
+// layouts at the widths of the 256 x 256 kernels).  Pieces past K are loaded
+// from a page of zeros, rows past M or N repeat the last one and are not
+// stored.
+constexpr int BN = 128;
+constexpr int KO_PITCH = 256;   // bytes of a K-outer row (128 columns)
+
+__device__ const uint4 g_zeros = {0, 0, 0, 0};
+
+__device__ __forceinline__ void load_lds(uint32_t lds, const uint16_t* src) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off"
+      :
+      : "s"(lds), "v"(src)
+      : "memory", "m0");
+}
+
+// One operand's share of the stage loads of a wavefront: R rows (K contiguous)
+// or columns (K-outer) of 32 k, 1 KB an instruction.
+template <int R, bool KO>
+struct Loader {
+  static constexpr int N = R / 64;   // instructions per wavefront and stage
+  const uint16_t* at[N];
+  int k[N];                          // the lane's first k of the stage
+  int64_t step;                      // elements from stage to stage
+  template <class Row>
+  __device__ __forceinline__ void init(const uint16_t* base, int64_t ld, int s0, int last, Row row) {
+    const int wave = wave_id(), lane = threadIdx.x & 63;
+    step = KO ? 32 * ld : 32;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int blk = i * 4 + wave;
+      if constexpr (KO) {
+        k[i] = 4 * blk + (lane >> 4);
+        const int c = (lane & 15) ^ fwd::kswz(k[i]);
+        at[i] = base + (32 * (int64_t)s0 + k[i]) * ld + min(row(8 * c), last - 8);
+      } else {
+        const int r = 16 * blk + (lane >> 2);
+        k[i] = 8 * ((lane & 3) ^ fwd::swz64(r));
+        at[i] = base + (int64_t)row(r) * ld + 32 * (int64_t)s0 + k[i];
+      }
+    }
+  }
+  // left: K minus the stage's first k; below 32 in a last, partial stage
+  __device__ __forceinline__ void issue(uint32_t lds, int left) {
+    const int wave = wave_id();
+    const uint16_t* const zero = reinterpret_cast<const uint16_t*>(&g_zeros);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      load_lds(lds + (i * 4 + wave) * 1024, left >= 32 || k[i] < left ? at[i] : zero);
+      at[i] += step;
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t ko_off(int nb) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
+  const int k = 8 * g + (j >> 2), n = nb + 4 * (j & 3);
+  return (uint32_t)(k * KO_PITCH + (((n >> 3) ^ fwd::kswz(k)) << 4) + ((n >> 2) & 1) * 8);
+}
+__device__ __forceinline__ bf16x8_t ko_read(const uint8_t* buf, uint32_t off) {
+  using namespace fwd;
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(buf + off));
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(buf + off + 4 * KO_PITCH));
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int BM>
+constexpr int ring() { return BM == 128 ? 5 : 6; }   // 80 or 72 KB: two workgroups a compute unit
+template <int BM>
+constexpr int stage_bytes() { return (BM + BN) * 64; }
+
+__device__ __forceinline__ f32x4_t load_bf16x4(const uint16_t* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return f32x4_t{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                 __uint_as_float(v.y & 0xFFFF0000u)};
+}
+
+// four columns of one row of the product's output from their full sums (GATE:
+// v = gate, u = up)
+template <int MODE>
+__device__ __forceinline__ void finish4(const Prod& a, int64_t m, int c, f32x4_t v, f32x4_t u) {
+  uint8_t* const out = reinterpret_cast<uint8_t*>(a.out);
+  if constexpr (MODE == GATE) {
+    if (a.aux) {
+      uint8_t* const aux = reinterpret_cast<uint8_t*>(a.aux);
+      store_sub<MOE_OUT_BF16>(aux, 2 * (int64_t)a.N, m, c, v);
+      store_sub<MOE_OUT_BF16>(aux, 2 * (int64_t)a.N, m, a.N + c, u);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = silu_f32(v[e]) * u[e];
+    store_sub<MOE_OUT_BF16>(out, a.N, m, c, v);
+  } else if constexpr (MODE == DGU) {
+    const f32x4_t g = load_bf16x4(a.res + m * 2 * a.N + c), w = load_bf16x4(a.res + m * 2 * a.N + a.N + c);
+    f32x4_t dg, du;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x, y;
+      swiglu_grad(g[e], w[e], v[e], x, y);
+      dg[e] = x;
+      du[e] = y;
+    }
+    store_sub<MOE_OUT_BF16>(out, 2 * (int64_t)a.N, m, c, dg);
+    store_sub<MOE_OUT_BF16>(out, 2 * (int64_t)a.N, m, a.N + c, du);
+  } else if constexpr (MODE == WGRAD) {
+    if (a.out_f32) {
+      store_sub<MOE_OUT_F32>(out, a.N, m, c, v);
+    } else {
+      store_sub<MOE_OUT_BF16>(out, a.N, m, c, v);
+    }
+  } else {
+    if (MODE == DOWN && a.res) v += load_bf16x4(a.res + m * a.ldr + c);
+    store_sub<MOE_OUT_BF16>(out, a.N, m, c, v);
+  }
+}
+
+template <int BM, int MODE>
+__device__ __forceinline__ void tile(const Prod& a, int block, uint8_t* lds) {
+  constexpr bool PKO = MODE == DGU || MODE == DX || MODE == WGRAD, QKO = MODE == WGRAD;
+  static_assert(!QKO || BM == 128, "K-outer rows are 128 columns");
+  constexpr int TM = BM / 32, TN = BN / 32, RING = ring<BM>(), STAGE = stage_bytes<BM>(), QOFF = BN * 64;
+  constexpr int NOUT = MODE == GATE ? BN / 2 : BN;   // output columns of the tile
+  // consecutive workgroups run on different XCDs; the m-tiles of one P tile
+  // follow each other on one XCD, so its L2 reads the weights once
+  const int xcd = block & 7, seq = block >> 3;
+  const int mt = seq % a.mtiles, unit = (seq / a.mtiles) * 8 + xcd;
   if (unit >= a.ntiles * a.S) return;
   const int nt = unit % a.ntiles, split = unit / a.ntiles;
-  const int m0 = mt * BM, n0 = nt * (GATED ? BN / 2 : BN);
-  const int steps = (a.K + 63) / 64;
-  const int s0 = (int)((int64_t)split * steps / a.S), s1 = (int)((int64_t)(split + 1) * steps / a.S);
+  const int m0 = mt * BM, n0 = nt * NOUT;
+  const int stages = (a.K + 31) / 32;
+  const int s0 = (int)((int64_t)split * stages / a.S), n = (int)((int64_t)(split + 1) * stages / a.S) - s0;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int r16 = lane & 15, g4 = lane >> 4;
   const int wm = wave & 1, wn = wave >> 1;
-  // loader: this thread's piece of row lr + 32 i
-  const int lr = threadIdx.x >> 3, lc = threadIdx.x & 7;
-  const uint16_t* xp[XR];
-  const uint16_t* wp[WR];
-#pragma unroll
-  for (int i = 0; i < XR; ++i) xp[i] = a.x + (int64_t)min(m0 + lr + 32 * i, a.T - 1) * a.ldx + 8 * lc;
-#pragma unroll
-  for (int i = 0; i < WR; ++i) {
-    const int r = lr + 32 * i;
-    int row;
-    if constexpr (GATED) {
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
+
+  Loader<BN, PKO> lp;
+  Loader<BM, QKO> lq;
+  lp.init(a.p, a.ldp, s0, a.N, [&](int r) {
+    if constexpr (PKO) {
+      return n0 + r;
+    } else if constexpr (MODE == GATE) {
+      // a wavefront's 64 rows: 32 gate rows, then the matching up rows
       const int w = r / (BN / 2), p = r % (BN / 2);
-      row = min(n0 + w * (BN / 4) + p % (BN / 4), a.N - 1) + (p < BN / 4 ? 0 : a.N);
+      return min(n0 + w * (BN / 4) + p % (BN / 4), a.N - 1) + (p < BN / 4 ? 0 : a.N);
     } else {
-      row = min(n0 + r, a.N - 1);
+      return min(n0 + r, a.N - 1);
     }
-    wp[i] = a.w + (int64_t)row * a.K + 8 * lc;
+  });
+  lq.init(a.q, a.ldq, s0, a.M, [&](int r) { return QKO ? m0 + r : min(m0 + r, a.M - 1); });
+  constexpr int LPW = Loader<BN, PKO>::N + Loader<BM, QKO>::N;
+  int issued = 0;   // stages
+  auto issue = [&]() {
+    const uint32_t b = base + (uint32_t)(issued % RING) * STAGE;
+    const int left = a.K - 32 * (s0 + issued);
+    lp.issue(b, left);
+    lq.issue(b + QOFF, left);
+    ++issued;
+  };
+  // fragment addresses within a stage
+  uint32_t po[TN], qo[TM];
+  const int slot = (g4 ^ fwd::swz64(r16)) << 4;
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    const int r = wn * (BN / 2) + 16 * i;
+    po[i] = PKO ? ko_off(r) : (uint32_t)((r + r16) * 64 + slot);
   }
-  uint4 xv[XR], wv[WR];
-  auto load = [&](int s) {
-    const int k = 64 * s;
-    const bool ok = k + 8 * lc < a.K;
 #pragma unroll
-    for (int i = 0; i < WR; ++i) wv[i] = ok ? *reinterpret_cast<const uint4*>(wp[i] + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < XR; ++i) xv[i] = ok ? *reinterpret_cast<const uint4*>(xp[i] + k) : make_uint4(0, 0, 0, 0);
-  };
-  auto put = [&](uint8_t* buf) {
-    const int o = lr * 128 + ((lc ^ (lr & 7)) << 4);
-#pragma unroll
-    for (int i = 0; i < WR; ++i) *reinterpret_cast<uint4*>(buf + o + i * 32 * 128) = wv[i];
-#pragma unroll
-    for (int i = 0; i < XR; ++i) *reinterpret_cast<uint4*>(buf + BN * 128 + o + i * 32 * 128) = xv[i];
-  };
+  for (int j = 0; j < TM; ++j) {
+    const int r = wm * (BM / 2) + 16 * j;
+    qo[j] = QOFF + (QKO ? ko_off(r) : (uint32_t)((r + r16) * 64 + slot));
+  }
   f32x4_t acc[TN][TM];
 #pragma unroll
   for (int i = 0; i < TN; ++i)
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  if (s0 < s1) {
-    load(s0);
-    put(lds[0]);
-    __syncthreads();
-    for (int s = s0; s < s1; ++s) {
-      const uint8_t* buf = lds[(s - s0) & 1];
-      if (s + 1 < s1) load(s + 1);
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const int slot = ((kk * 4 + g4) ^ (r16 & 7)) << 4;
-        uint4 fw[TN], fx[TM];
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-          fw[i] = *reinterpret_cast<const uint4*>(buf + (wn * (BN / 2) + i * 16 + r16) * 128 + slot);
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-          fx[j] = *reinterpret_cast<const uint4*>(buf + BN * 128 + (wm * (BM / 2) + j * 16 + r16) * 128 + slot);
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-          for (int j = 0; j < TM; ++j) acc[i][j] = mfma(fw[i], fx[j], acc[i][j]);
-      }
-      if (s + 1 < s1) put(lds[(s + 1 - s0) & 1]);
-      __syncthreads();
+  for (int i = 0; i < RING - 1 && i < n; ++i) issue();
+  int cur = 0;
+  for (int s = 0; s < n; ++s) {
+    // this wavefront's loads of stage s have landed, its reads of stage s - 1
+    // are done; behind the barrier, everybody's
+    const int later = min(RING - 2, n - 1 - s);
+    __builtin_amdgcn_sched_barrier(0);
+    switch (later) {
+      case 0: MOE_WAIT_VMCNT(0); break;
+      case 1: MOE_WAIT_VMCNT(LPW); break;
+      case 2: MOE_WAIT_VMCNT(2 * LPW); break;
+      case 3: MOE_WAIT_VMCNT(3 * LPW); break;
+      default: MOE_WAIT_VMCNT((RING - 2) * LPW); break;
     }
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + RING - 1 < n) issue();        // into the buffer of stage s - 1
+    const uint8_t* const buf = lds + cur * STAGE;
+    cur = cur + 1 == RING ? 0 : cur + 1;
+    bf16x8_t fp[TN], fq[TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      if constexpr (PKO) {
+        fp[i] = ko_read(buf, po[i]);
+      } else {
+        fp[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4*>(buf + po[i]));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      if constexpr (QKO) {
+        fq[j] = ko_read(buf, qo[j]);
+      } else {
+        fq[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4*>(buf + qo[j]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[i], fq[j], acc[i][j], 0, 0, 0);
   }
-  // lane: token r16 of each 16, four consecutive columns from 4 g4
+  // lane: row r16 of each 16, four consecutive columns from 4 g4
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
-    const int t = m0 + wm * (BM / 2) + j * 16 + r16;
-    if (t >= a.T) continue;
-    if constexpr (GATED) {
+    const int m = m0 + wm * (BM / 2) + j * 16 + r16;
+    if (m >= a.M) continue;
+    constexpr int NI = MODE == GATE ? TN / 2 : TN;
 #pragma unroll
-      for (int i = 0; i < TN / 2; ++i) {
-        const int c = n0 + wn * (BN / 4) + i * 16 + 4 * g4;
-        if (c >= a.N) continue;
-        const f32x4_t g = acc[i][j], u = acc[i + TN / 2][j];
-        if (a.part) {
-          float* const o = a.part + ((int64_t)split * a.T + t) * 2 * a.N;
-          *reinterpret_cast<f32x4_t*>(o + c) = g;
-          *reinterpret_cast<f32x4_t*>(o + a.N + c) = u;
-        } else {
-          uint8_t* const aux = reinterpret_cast<uint8_t*>(a.aux);
-          if (aux) {
-            store_sub<MOE_OUT_BF16>(aux, 2 * (int64_t)a.N, t, c, g);
-            store_sub<MOE_OUT_BF16>(aux, 2 * (int64_t)a.N, t, a.N + c, u);
-          }
-          f32x4_t h;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = silu_f32(g[e]) * u[e];
-          store_sub<MOE_OUT_BF16>(reinterpret_cast<uint8_t*>(a.out), a.N, t, c, h);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        const int c = n0 + wn * (BN / 2) + i * 16 + 4 * g4;
-        if (c >= a.N) continue;
-        f32x4_t v = acc[i][j];
-        if (a.part) {
-          *reinterpret_cast<f32x4_t*>(a.part + ((int64_t)split * a.T + t) * a.N + c) = v;
-        } else {
-          if (a.res) {
-            const uint16_t* r = a.res + t * a.ldr + c;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += bf16_bits_to_f32(r[e]);
-          }
-          store_sub<MOE_OUT_BF16>(reinterpret_cast<uint8_t*>(a.out), a.N, t, c, v);
-        }
+    for (int i = 0; i < NI; ++i) {
+      const int c = n0 + wn * (NOUT / 2) + i * 16 + 4 * g4;
+      if (c >= a.N) continue;
+      const f32x4_t v = acc[i][j], u = MODE == GATE ? acc[i + TN - NI][j] : v;
+      if (a.part) {
+        float* const o = a.part + ((int64_t)split * a.M + m) * (MODE == GATE ? 2 : 1) * a.N + c;
+        *reinterpret_cast<f32x4_t*>(o) = v;
+        if constexpr (MODE == GATE) *reinterpret_cast<f32x4_t*>(o + a.N) = u;
+      } else {
+        finish4<MODE>(a, m, c, v, u);
       }
     }
   }
 }
 
+template <int BM, int MODE>
+__global__ __launch_bounds__(256, 2) void tile_kernel(Prod a) {
+  __shared__ __align__(1024) uint8_t lds[ring<BM>() * stage_bytes<BM>()];
+  tile<BM, MODE>(a, (int)blockIdx.x, lds);
+}
+
+// What follows dgu in the backward, in one launch: dx and both weight
+// gradients are independent, and together they fill the chip.
+struct Backward {
+  Prod dx, dw1, dw2;
+  int blocks_dx, blocks_dw1;
+};
+template <int BM>
+__global__ __launch_bounds__(256, 2) void backward_kernel(Backward a) {
+  __shared__ __align__(1024) uint8_t lds[ring<128>() * stage_bytes<128>()];
+  int b = (int)blockIdx.x;
+  if (b < a.blocks_dx) {
+    tile<BM, DX>(a.dx, b, lds);
+    return;
+  }
+  b -= a.blocks_dx;
+  const bool first = b < a.blocks_dw1;
+  tile<128, WGRAD>(first ? a.dw1 : a.dw2, first ? b : b - a.blocks_dw1, lds);
+}
+
 // The partial sums of the S splits, added in split order, through the
 // product's epilogue; four columns a thread.
-template <bool GATED>
-__global__ __launch_bounds__(256) void join_kernel(ProdArgs a) {
+template <int MODE>
+__global__ __launch_bounds__(256) void join_kernel(Prod a) {
   const int nq = a.N / 4;
-  const int64_t total = (int64_t)a.T * nq;
-  const int ld = GATED ? 2 * a.N : a.N;
-  const int64_t plane = (int64_t)a.T * ld;
+  const int64_t total = (int64_t)a.M * nq;
+  const int ld = MODE == GATE ? 2 * a.N : a.N;
+  const int64_t plane = (int64_t)a.M * ld;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / nq;
-    const int c = 4 * (int)(i - t * nq);
-    const float* p = a.part + t * ld + c;
+    const int64_t m = i / nq;
+    const int c = 4 * (int)(i - m * nq);
+    const float* p = a.part + m * ld + c;
     f32x4_t v = *reinterpret_cast<const f32x4_t*>(p), u = v;
-    if constexpr (GATED) u = *reinterpret_cast<const f32x4_t*>(p + a.N);
+    if constexpr (MODE == GATE) u = *reinterpret_cast<const f32x4_t*>(p + a.N);
 #pragma unroll 4
     for (int s = 1; s < a.S; ++s) {
       v += *reinterpret_cast<const f32x4_t*>(p + s * plane);
-      if constexpr (GATED) u += *reinterpret_cast<const f32x4_t*>(p + s * plane + a.N);
+      if constexpr (MODE == GATE) u += *reinterpret_cast<const f32x4_t*>(p + s * plane + a.N);
     }
-    if constexpr (GATED) {
-      if (a.aux) {
-        uint8_t* const aux = reinterpret_cast<uint8_t*>(a.aux);
-        store_sub<MOE_OUT_BF16>(aux, ld, t, c, v);
-        store_sub<MOE_OUT_BF16>(aux, ld, t, a.N + c, u);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = silu_f32(v[e]) * u[e];
-    } else if (a.res) {
-      const uint16_t* r = a.res + t * a.ldr + c;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += bf16_bits_to_f32(r[e]);
-    }
-    store_sub<MOE_OUT_BF16>(reinterpret_cast<uint8_t*>(a.out), a.N, t, c, v);
+    finish4<MODE>(a, m, c, v, u);
   }
 }
 
@@ -317,48 +455,70 @@ struct Plan {
   int BM, S;
 };
 
-// How one product [T, K] x [N or 2N, K] runs.
-Plan choose_form(int64_t T, int N, int K, bool gated, bool strided) {
+// How a product of M rows, N output columns (GATE: N pairs) and contraction K
+// runs.  `many`: whether the 256 x 256 kernels take its shapes.
+Plan choose_form(Mode mode, int64_t M, int N, int K, bool many) {
   const int cus = moe_host::device_cu_count();
-  if (T <= 16) return {FEW, 0, 1};
-  const int64_t big = ((T + 255) / 256) * ((N + (gated ? 127 : 255)) / (gated ? 128 : 256));
-  if (!strided && K % 64 == 0 && 4 * big >= 3 * (int64_t)cus) return {MANY, 0, 1};
-  const int BM = T <= 64 ? 64 : 128;
-  const int64_t tiles = ((T + BM - 1) / BM) * ((N + (gated ? 63 : 127)) / (gated ? 64 : 128));
-  const int steps = (K + 63) / 64;
-  const int S = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps / 4), 2 * cus / tiles));
+  const int nout = mode == GATE ? BN / 2 : BN;
+  if (M <= 16 && (mode == GATE || mode == DOWN)) return {FEW, 0, 1};
+  const int64_t big = ((M + 255) / 256) * ((N + 2 * nout - 1) / (2 * nout));
+  if (many && 4 * big >= 3 * (int64_t)cus) return {MANY, 0, 1};
+  const int BM = M <= 64 && mode != WGRAD ? 64 : 128;
+  const int64_t tiles = std::max<int64_t>(1, (M + BM - 1) / BM) * ((N + nout - 1) / nout);
+  const int stages = (K + 31) / 32;
+  const int S = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, stages / 8), 2 * cus / tiles));
   return {TILES, BM, S};
 }
 
-size_t part_bytes(const Plan& p, int64_t T, int N, bool gated) {
+size_t part_bytes(Mode mode, const Plan& p, int64_t M, int N) {
   if (p.form == MANY) return fwd_split_workspace_bytes();
-  if (p.form == TILES && p.S > 1) return (size_t)p.S * (size_t)T * (size_t)(gated ? 2 * N : N) * 4;
+  if (p.form == TILES && p.S > 1) return (size_t)p.S * (size_t)M * (size_t)(mode == GATE ? 2 * N : N) * 4;
   return 0;
 }
 
 moe_status_t status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
-template <bool GATED>
-moe_status_t run_tiles(ProdArgs a, const Plan& p, hipStream_t s) {
-  constexpr int BN = 128;
+// sets a product's grid up; its workgroups
+int64_t lay_out(Mode mode, Prod& a, const Plan& p) {
+  const int nout = mode == GATE ? BN / 2 : BN;
   a.S = p.S;
   if (p.S == 1) a.part = nullptr;
-  a.mtiles = (a.T + p.BM - 1) / p.BM;
-  a.ntiles = (a.N + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
-  const int64_t units = (int64_t)a.ntiles * a.S;
-  const dim3 grid((unsigned)(8 * a.mtiles * ((units + 7) / 8)));
+  a.mtiles = (a.M + p.BM - 1) / p.BM;
+  a.ntiles = (a.N + nout - 1) / nout;
+  return 8 * (int64_t)a.mtiles * (((int64_t)a.ntiles * a.S + 7) / 8);
+}
+
+template <int MODE>
+moe_status_t run_tiles(Prod a, const Plan& p, hipStream_t s) {
+  const int64_t blocks = lay_out((Mode)MODE, a, p);
+  if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (p.BM == 64) {
-    hipLaunchKernelGGL((tile_kernel<64, BN, GATED>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<64, MODE>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   } else {
-    hipLaunchKernelGGL((tile_kernel<128, BN, GATED>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<128, MODE>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   }
   if (status() != MOE_OK) return MOE_ERR_HIP;
   if (p.S > 1) {
-    const int64_t total = (int64_t)a.T * (a.N / 4);
-    const int64_t blocks = std::min<int64_t>((total + 255) / 256, 16 * (int64_t)moe_host::device_cu_count());
-    hipLaunchKernelGGL((join_kernel<GATED>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+    const int64_t total = (int64_t)a.M * (a.N / 4);
+    const int64_t nb = std::min<int64_t>((total + 255) / 256, 16 * (int64_t)moe_host::device_cu_count());
+    hipLaunchKernelGGL((join_kernel<MODE>), dim3((unsigned)nb), dim3(256), 0, s, a);
   }
   return status();
+}
+
+Prod product(const uint16_t* p, int64_t ldp, const uint16_t* q, int64_t ldq, void* out, int64_t M, int N, int K,
+             float* part) {
+  Prod a{};
+  a.p = p;
+  a.ldp = ldp;
+  a.q = q;
+  a.ldq = ldq;
+  a.out = reinterpret_cast<uint16_t*>(out);
+  a.M = (int)M;
+  a.N = N;
+  a.K = K;
+  a.part = part;
+  return a;
 }
 
 GGArgs one_group(const void* A, const void* B, void* C, void* aux, int64_t T, int N, int K, const int32_t* rows,
@@ -379,6 +539,20 @@ GGArgs one_group(const void* A, const void* B, void* C, void* aux, int64_t T, in
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// the backward's first product, and whether the others (dx, dw1p, dw2) run
+// as the one launch of tiles
+struct BackwardPlan {
+  Plan dgu;
+  bool tiles;
+  int bm_dx;
+};
+BackwardPlan plan_backward(int64_t T, int d, int f) {
+  const int64_t cus = moe_host::device_cu_count();
+  const bool many = d % 64 == 0 && f % 32 == 0;
+  const int64_t m = (T + 255) / 256, big = m * ((d + 255) / 256);
+  return {choose_form(DGU, T, f, d, many), !many || 4 * big < 3 * cus, T <= 64 ? 64 : 128};
+}
+
 }  // namespace ffn
 }  // namespace moe
 
@@ -388,8 +562,8 @@ using namespace moe::ffn;
 // Workspace: the row count (device), h where the caller keeps none, and the
 // larger of the two products' partial sums.
 extern "C" size_t moe_gated_ffn_ws_impl(int64_t T, int32_t d, int32_t f, int keep, int strided) {
-  const size_t a = part_bytes(choose_form(T, f, d, true, strided), T, f, true);
-  const size_t b = part_bytes(choose_form(T, d, f, false, false), T, d, false);
+  const size_t a = part_bytes(GATE, choose_form(GATE, T, f, d, !strided && d % 64 == 0), T, f);
+  const size_t b = part_bytes(DOWN, choose_form(DOWN, T, d, f, f % 64 == 0), T, d);
   return 256 + (keep ? 0 : up256((size_t)T * f * 2)) + std::max(a, b);
 }
 
@@ -404,48 +578,31 @@ extern "C" moe_status_t moe_gated_ffn_launch(const uint16_t* x, int64_t ldx, con
     w += up256((size_t)T * f * 2);
   }
   float* const part = reinterpret_cast<float*>(w);
-  const bool strided = ldx != d;
-  const Plan p1 = choose_form(T, f, d, true, strided), p2 = choose_form(T, d, f, false, false);
+  const Plan p1 = choose_form(GATE, T, f, d, ldx == d && d % 64 == 0), p2 = choose_form(DOWN, T, d, f, f % 64 == 0);
   if (p1.form == MANY || p2.form == MANY) {
     hipLaunchKernelGGL(set_rows_kernel, dim3(1), dim3(1), 0, s, rows, (int32_t)T);
     if (ffn::status() != MOE_OK) return MOE_ERR_HIP;
   }
-  ProdArgs a{};
-  a.x = x;
-  a.ldx = ldx;
-  a.w = w1p;
-  a.out = h;
+  Prod a = product(w1p, d, x, ldx, h, T, f, d, part);
   a.aux = gu;
-  a.part = part;
-  a.T = (int)T;
-  a.N = f;
-  a.K = d;
   moe_status_t st;
   if (p1.form == FEW) {
     hipLaunchKernelGGL((few_tokens_kernel<1, true>), dim3((unsigned)((f + 7) / 8)), dim3(kFewWaves * 64), 0, s, a);
     st = ffn::status();
   } else if (p1.form == TILES) {
-    st = run_tiles<true>(a, p1, s);
+    st = run_tiles<GATE>(a, p1, s);
   } else {
     st = launch_fwd(one_group(x, w1p, h, gu, T, 2 * f, d, rows, part), MOE_EPI_SWIGLU, 0, MOE_B_NK, s);
   }
   if (st != MOE_OK) return st;
-  ProdArgs b{};
-  b.x = h;
-  b.ldx = f;
-  b.w = w2;
+  Prod b = product(w2, f, h, f, y, T, d, f, part);
   b.res = res;
   b.ldr = ldr;
-  b.out = y;
-  b.part = part;
-  b.T = (int)T;
-  b.N = d;
-  b.K = f;
   if (p2.form == FEW) {
     hipLaunchKernelGGL((few_tokens_kernel<1, false>), dim3((unsigned)((d + 15) / 16)), dim3(kFewWaves * 64), 0, s, b);
     return ffn::status();
   }
-  if (p2.form == TILES) return run_tiles<false>(b, p2, s);
+  if (p2.form == TILES) return run_tiles<DOWN>(b, p2, s);
   GGArgs g = one_group(h, w2, y, const_cast<uint16_t*>(res), T, d, f, rows, part);
   if (res) {
     g.ld_aux = ldr;
@@ -454,7 +611,10 @@ extern "C" moe_status_t moe_gated_ffn_launch(const uint16_t* x, int64_t ldx, con
   return launch_fwd(g, MOE_EPI_NONE, 0, MOE_B_NK, s);
 }
 
-extern "C" size_t moe_gated_ffn_backward_ws_impl(void) { return 256 + fwd_split_workspace_bytes(); }
+extern "C" size_t moe_gated_ffn_backward_ws_impl(int64_t T, int32_t d, int32_t f) {
+  const BackwardPlan p = plan_backward(T, d, f);
+  return 256 + std::max(part_bytes(DGU, p.dgu, T, f), p.tiles ? (size_t)0 : fwd_split_workspace_bytes());
+}
 
 extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const uint16_t* x, const uint16_t* gu,
                                                       const uint16_t* h, const uint16_t* w1p, const uint16_t* w2,
@@ -462,15 +622,45 @@ extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const 
                                                       void* dw1p, void* dw2, int out_f32, void* ws, hipStream_t s) {
   int32_t* const rows = reinterpret_cast<int32_t*>(ws);
   float* const part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + 256);
-  hipLaunchKernelGGL(set_rows_kernel, dim3(1), dim3(1), 0, s, rows, (int32_t)T);
-  moe_status_t st = ffn::status();
-  // dgu = swiglu'(gu, dy W2), dx = dgu W1p
-  if (st == MOE_OK && T > 0)
-    st = launch_fwd(one_group(dy, w2, dgu, const_cast<uint16_t*>(gu), T, f, d, rows, part), MOE_EPI_SWIGLU_BWD, 0,
-                    MOE_B_KN, s);
-  if (st == MOE_OK && T > 0)
-    st = launch_fwd(one_group(dgu, w1p, dx, nullptr, T, d, 2 * f, rows, part), MOE_EPI_NONE, 0, MOE_B_KN, s);
-  // dW1p = dgu^T x, dW2 = dy^T h
+  const BackwardPlan p = plan_backward(T, d, f);
+  moe_status_t st = MOE_OK;
+  if (p.dgu.form == MANY || !p.tiles) {
+    hipLaunchKernelGGL(set_rows_kernel, dim3(1), dim3(1), 0, s, rows, (int32_t)T);
+    st = ffn::status();
+    if (st != MOE_OK) return st;
+  }
+  // dgu = swiglu'(gu, dy W2)
+  if (T > 0) {
+    if (p.dgu.form == MANY) {
+      st = launch_fwd(one_group(dy, w2, dgu, const_cast<uint16_t*>(gu), T, f, d, rows, part), MOE_EPI_SWIGLU_BWD, 0,
+                      MOE_B_KN, s);
+    } else {
+      Prod a = product(w2, f, dy, d, dgu, T, f, d, part);
+      a.res = gu;
+      st = run_tiles<DGU>(a, p.dgu, s);
+    }
+    if (st != MOE_OK) return st;
+  }
+  // dx = dgu W1p, dW1p = dgu^T x, dW2 = dy^T h
+  if (p.tiles) {
+    Backward b;
+    b.dx = product(w1p, d, dgu, 2 * (int64_t)f, dx, T, d, 2 * f, nullptr);
+    b.dw1 = product(x, d, dgu, 2 * (int64_t)f, dw1p, 2 * f, d, (int)T, nullptr);
+    b.dw2 = product(h, f, dy, d, dw2, d, f, (int)T, nullptr);
+    b.dw1.out_f32 = b.dw2.out_f32 = out_f32;
+    const int64_t n0 = T > 0 ? lay_out(DX, b.dx, {TILES, p.bm_dx, 1}) : 0;
+    const int64_t n1 = lay_out(WGRAD, b.dw1, {TILES, 128, 1}), n2 = lay_out(WGRAD, b.dw2, {TILES, 128, 1});
+    if (n0 + n1 + n2 > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    b.blocks_dx = (int)n0;
+    b.blocks_dw1 = (int)n1;
+    if (p.bm_dx == 64) {
+      hipLaunchKernelGGL((backward_kernel<64>), dim3((unsigned)(n0 + n1 + n2)), dim3(256), 0, s, b);
+    } else {
+      hipLaunchKernelGGL((backward_kernel<128>), dim3((unsigned)(n0 + n1 + n2)), dim3(256), 0, s, b);
+    }
+    return ffn::status();
+  }
+  st = launch_fwd(one_group(dgu, w1p, dx, nullptr, T, d, 2 * f, rows, part), MOE_EPI_NONE, 0, MOE_B_KN, s);
   if (st == MOE_OK) {
     GGArgs g = one_group(dgu, x, dw1p, nullptr, T, d, 0, rows, nullptr);
     g.M = 2 * f;

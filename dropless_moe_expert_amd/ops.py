@@ -106,7 +106,7 @@ def load_library(path: str = LIB_PATH, require_gpu: bool = True):
                                                         P]),
             "moe_gated_ffn_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
             "moe_gated_ffn": (ctypes.c_int, [P, i64, P, P, P, i64, i64, i32, i32, P, P, P, P, sz, P]),
-            "moe_gated_ffn_backward_workspace_bytes": (sz, []),
+            "moe_gated_ffn_backward_workspace_bytes": (sz, [i64, i32, i32]),
             "moe_gated_ffn_backward": (ctypes.c_int, [P, P, P, P, P, P, i64, i32, i32, i32, P, P, P, P, P, sz, P]),
             "moe_adamw_step": (ctypes.c_int, [P, i32, P, P, P, P]),
             "moe_bench_mfma_flops": (i64, [i64, i32]),
@@ -847,8 +847,8 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, saved: dict, w1p: torc
     dx = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
     dw1p = torch.empty((2 * f, d), dtype=out_dtype, device=dev)
     dw2 = torch.empty((d, f), dtype=out_dtype, device=dev)
-    need = lib().moe_gated_ffn_backward_workspace_bytes()
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    need = lib().moe_gated_ffn_backward_workspace_bytes(T, d, f)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     _invoke(dev, "moe_gated_ffn_backward", _ptr(dy), _ptr(x), _ptr(saved["gu"]), _ptr(saved["h"]), _ptr(w1p), _ptr(w2),
             T, d, f, MOE_OUT_F32 if out_dtype == torch.float32 else MOE_OUT_BF16, _ptr(dgu), _ptr(dx), _ptr(dw1p),
             _ptr(dw2), _ptr(ws), need)

@@ -554,12 +554,13 @@ moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, 
  *   dh = dy W2, dgu = SwiGLU's backward of (gu, dh), dx = dgu W1p,
  *   dw1p = dgu^T x [2f, d], dw2 = dy^T h [d, f]   (out_dtype bf16 or fp32)
  * dgu bf16 [T, 2f] is an output too.  All operands contiguous and 16-byte
- * aligned.  ws: moe_gated_ffn_backward_workspace_bytes(), 256-byte aligned.
- * T = 0 gives zero weight gradients.  The weight gradients take two of the 64
- * queue slots of RAGGED_K grouped_gemm: what is said there about calls in
- * flight and about one graph on two streams holds here.  Limits: d % 64 == 0,
- * f % 32 == 0, else as the forward. */
-size_t moe_gated_ffn_backward_workspace_bytes(void);
+ * aligned.  ws: moe_gated_ffn_backward_workspace_bytes(T, d, f), 256-byte
+ * aligned; calls in flight together must not share it.  T = 0 gives zero
+ * weight gradients.  Sizes as the forward (d % 64 == 0 and f % 32 == 0 let many
+ * tokens run on the kernels of the grouped products; their weight gradients
+ * take two of the 64 queue slots of RAGGED_K grouped_gemm: what is said there
+ * about calls in flight and about one graph on two streams holds here). */
+size_t moe_gated_ffn_backward_workspace_bytes(int64_t T, int32_t d, int32_t f);
 moe_status_t moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* gu, const uint16_t* h,
                                     const uint16_t* w1p, const uint16_t* w2, int64_t T, int32_t d, int32_t f,
                                     int32_t out_dtype, uint16_t* dgu, uint16_t* dx, void* dw1p, void* dw2, void* ws,

@@ -38,7 +38,7 @@ moe_status_t moe_gated_ffn_launch(const uint16_t*, int64_t, const uint16_t*, con
   ++g_launches;
   return MOE_OK;
 }
-size_t moe_gated_ffn_backward_ws_impl(void) { return 256; }
+size_t moe_gated_ffn_backward_ws_impl(int64_t, int32_t, int32_t) { return 256; }
 moe_status_t moe_gated_ffn_backward_launch(const uint16_t*, const uint16_t*, const uint16_t*, const uint16_t*,
                                            const uint16_t*, const uint16_t*, int64_t, int32_t, int32_t, uint16_t*,
                                            uint16_t*, void*, void*, int, void*, hipStream_t) {
@@ -100,6 +100,7 @@ int main() {
   check(moe_add_rmsnorm_backward_workspace_bytes(INT32_MAX, 32768) == (size_t)512 * 32768 * 4, "norm ws");
   check(moe_gated_ffn_workspace_bytes(INT64_MAX, 64, 64, 0, 0) == 0, "ffn ws, T");
   check(moe_gated_ffn_workspace_bytes(4, INT32_MAX - 7, 64, 0, 0) == 0, "ffn ws, d");
+  check(moe_gated_ffn_backward_workspace_bytes(INT64_MAX, 64, 64) == 0, "ffn backward ws, T");
   const int before = g_launches;
   check(moe_gated_ffn(u16(P), 64, u16(P), u16(P), nullptr, 0, INT64_MAX, 64, 64, nullptr, nullptr, u16(2 * P), ws,
                       SIZE_MAX, nullptr) == MOE_ERR_UNSUPPORTED, "ffn, T");

@@ -194,8 +194,10 @@ def test_ffn_backward_refusals(L):
     for name in ("dy", "x", "gu", "h", "w1", "w2", "dgu", "dx", "dw1", "dw2"):
         assert _ffn_bwd(L, **{name: None}) == INVALID, name
         assert _ffn_bwd(L, **{name: FAKE + 8}) == ALIGN, name
-    assert _ffn_bwd(L, d=72) == UNSUPPORTED and _ffn_bwd(L, f=40) == UNSUPPORTED and _ffn_bwd(L, dt=4) == UNSUPPORTED
-    need = L.moe_gated_ffn_backward_workspace_bytes()
+    assert _ffn_bwd(L, d=60) == UNSUPPORTED and _ffn_bwd(L, f=12) == UNSUPPORTED and _ffn_bwd(L, dt=4) == UNSUPPORTED
+    assert _ffn_bwd(L, T=-1) == INVALID and _ffn_bwd(L, T=1 << 31) == UNSUPPORTED
+    need = L.moe_gated_ffn_backward_workspace_bytes(4, 64, 32)
+    assert need >= 256 and L.moe_gated_ffn_backward_workspace_bytes(4, 60, 32) == 0
     assert _ffn_bwd(L, n=need - 1) == WS and _ffn_bwd(L, ws=FAKE + 16) == ALIGN
 
 

@@ -295,7 +295,9 @@ def _check_ffn_bwd(ops, dy, x, saved, w1, w2, out_dtype):
 
 
 @pytest.mark.parametrize("T,d,f", [(1, 64, 32), (1, 128, 64), (2, 64, 96), (33, 128, 160), (255, 320, 64), (257, 64, 288),
-                                   (300, 1024, 256), (1000, 256, 768), (1100, 2112, 64)])
+                                   (300, 1024, 256), (1000, 256, 768), (1100, 2112, 64),
+                                   (1, 8, 8), (3, 72, 40), (65, 200, 136), (130, 1032, 24), (31, 8, 264), (6200, 2112, 64),
+                                   (6200, 640, 2304)])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 def test_gated_ffn_backward(ops, T, d, f, out_dtype):
     say("gated_ffn_backward", T, d, f, out_dtype)
