@@ -144,6 +144,8 @@ moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, 
   if (!x || !w1p || !w2 || !y || (gu && !h) || y == x) return MOE_ERR_INVALID_ARG;
   if (ldx < d || (res && ldres < d) || (res == y && res && ldres != d)) return MOE_ERR_INVALID_ARG;
   if (ldx % 8 || (res && ldres % 8)) return MOE_ERR_ALIGNMENT;
+  // 128 rows' byte offsets stay in 32 bits
+  if (ldx > (1 << 23) || (res && ldres > (1 << 23))) return MOE_ERR_UNSUPPORTED;
   if (!aligned(x, 16) || !aligned(w1p, 16) || !aligned(w2, 16) || !aligned(res, 16) || !aligned(h, 16) ||
       !aligned(gu, 16) || !aligned(y, 16))
     return MOE_ERR_ALIGNMENT;

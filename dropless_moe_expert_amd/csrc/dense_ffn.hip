@@ -17,6 +17,7 @@
 //  * many: the persistent 256 x 256 kernels of the grouped products
 //    (gg_bf16.hip) with one group.
 #include <algorithm>
+#include <type_traits>
 
 #include "dense_args.h"
 #include "gg_pipeline.h"
@@ -148,21 +149,37 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(Prod a) {
 
 // ------------------------------------------------------------------ tiles
 // One BM x 128 tile (m x n) of a product, over one range of K.  K is staged
-// 32 at a time in a ring of LDS buffers filled by direct-to-LDS loads, RING - 1
-// stages ahead of the stage being multiplied: the weights stream from HBM, and
-// what is in flight bounds their rate (two workgroups a compute unit).  Four
-// wavefronts, 2 (m) x 2 (n).  An operand with K contiguous is 64-byte rows,
-// 16-byte slots swizzled by row; a K-outer one is 32 rows of 256 bytes whose
-// fragments come through the LDS transpose read (gg_pipeline.h has both
-// layouts at the widths of the 256 x 256 kernels).  Pieces past K are loaded
-// from a page of zeros, rows past M or N repeat the last one and are not
-// stored.
+// 64 at a time in a ring of LDS buffers (nearly all of LDS) filled by
+// direct-to-LDS loads, RING stages ahead: the weights stream from
+// HBM, and what is in flight bounds their rate.  64 deep, because a stage's row
+// piece is then a whole 128-byte line: with 32 deep stages the L2 served twice
+// the requests and the weights came at half the rate.  Eight wavefronts, 2 (m)
+// x 2 (n) x 2 halves of every stage's K, so that a wavefront's tile is 64 x 64
+// and reads the fewest LDS bytes an MFMA; the halves' sums meet in LDS at the
+// end.  The fragments of the next stage are read while the present one is
+// multiplied.  An operand with K contiguous is 128-byte rows, 16-byte slots
+// swizzled by row; a K-outer one is 64 rows of 256 bytes whose fragments come
+// through the LDS transpose read (gg_pipeline.h has both layouts at the widths
+// of the 256 x 256 kernels).  Pieces past K are loaded from a page of zeros,
+// rows past M or N repeat the last one and are not stored.
 constexpr int BN = 128;
 constexpr int KO_PITCH = 256;   // bytes of a K-outer row (128 columns)
 
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
 
-__device__ __forceinline__ void load_lds(uint32_t lds, const uint16_t* src) {
+// 16 bytes a lane into the 1 KB of LDS at lds: from base + off bytes, or from
+// each lane's own address (as inline asm: the compiler then adds no wait of its
+// own; M0, the LDS base, is not used by anything else it emits here)
+__device__ __forceinline__ void load_lds(uint32_t lds, const uint16_t* base, uint32_t off) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds(uint32_t lds, const uint8_t* src) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
       "s_nop 0\n\t"
@@ -173,40 +190,47 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const uint16_t* src) {
 }
 
 // One operand's share of the stage loads of a wavefront: R rows (K contiguous)
-// or columns (K-outer) of 32 k, 1 KB an instruction.
+// or columns (K-outer) of 64 k, 1 KB an instruction.
 template <int R, bool KO>
 struct Loader {
   static constexpr int N = R / 64;   // instructions per wavefront and stage
-  const uint16_t* at[N];
-  int k[N];                          // the lane's first k of the stage
+  const uint16_t* base;              // the next stage's first element (uniform)
   int64_t step;                      // elements from stage to stage
+  uint32_t off[N];                   // this lane's pieces, bytes from base
+  int k[N];                          // and their first k within the stage
+  // origin: the operand's first element of the tile at k = 0; row(r): the row
+  // (K contiguous) or column (K-outer) r of the tile, counted from origin
   template <class Row>
-  __device__ __forceinline__ void init(const uint16_t* base, int64_t ld, int s0, int last, Row row) {
+  __device__ __forceinline__ void init(const uint16_t* origin, int64_t ld, int s0, Row row) {
     const int wave = wave_id(), lane = threadIdx.x & 63;
-    step = KO ? 32 * ld : 32;
+    step = KO ? 64 * ld : 64;
+    base = origin + step * s0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int blk = i * 4 + wave;
+      const int blk = i * 8 + wave;
       if constexpr (KO) {
         k[i] = 4 * blk + (lane >> 4);
-        const int c = (lane & 15) ^ fwd::kswz(k[i]);
-        at[i] = base + (32 * (int64_t)s0 + k[i]) * ld + min(row(8 * c), last - 8);
+        off[i] = (uint32_t)(k[i] * ld + row(8 * ((lane & 15) ^ fwd::kswz(k[i])))) * 2u;
       } else {
-        const int r = 16 * blk + (lane >> 2);
-        k[i] = 8 * ((lane & 3) ^ fwd::swz64(r));
-        at[i] = base + (int64_t)row(r) * ld + 32 * (int64_t)s0 + k[i];
+        const int r = 8 * blk + (lane >> 3);
+        k[i] = 8 * ((lane & 7) ^ (r & 7));
+        off[i] = (uint32_t)(row(r) * ld + k[i]) * 2u;
       }
     }
   }
-  // left: K minus the stage's first k; below 32 in a last, partial stage
-  __device__ __forceinline__ void issue(uint32_t lds, int left) {
+  __device__ __forceinline__ void issue(uint32_t lds) {
     const int wave = wave_id();
-    const uint16_t* const zero = reinterpret_cast<const uint16_t*>(&g_zeros);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      load_lds(lds + (i * 4 + wave) * 1024, left >= 32 || k[i] < left ? at[i] : zero);
-      at[i] += step;
-    }
+    for (int i = 0; i < N; ++i) load_lds(lds + (i * 8 + wave) * 1024, base, off[i]);
+    base += step;
+  }
+  // the last stage of K, of which `left` < 64 are there
+  __device__ __forceinline__ void issue_partial(uint32_t lds, int left) {
+    const int wave = wave_id();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      load_lds(lds + (i * 8 + wave) * 1024, k[i] < left ? reinterpret_cast<const uint8_t*>(base) + off[i]
+                                                        : reinterpret_cast<const uint8_t*>(&g_zeros));
   }
 };
 
@@ -223,9 +247,12 @@ __device__ __forceinline__ bf16x8_t ko_read(const uint8_t* buf, uint32_t off) {
 }
 
 template <int BM>
-constexpr int ring() { return BM == 128 ? 5 : 6; }   // 80 or 72 KB: two workgroups a compute unit
+constexpr int ring() { return BM == 128 ? 4 : 6; }   // 128 or 144 KB: one workgroup a compute unit
 template <int BM>
-constexpr int stage_bytes() { return (BM + BN) * 64; }
+constexpr int stage_bytes() { return (BM + BN) * 128; }
+template <int BM>
+constexpr int tile_lds() { return ring<BM>() * stage_bytes<BM>(); }
+constexpr int kTileThreads = 512;
 
 __device__ __forceinline__ f32x4_t load_bf16x4(const uint16_t* p) {
   const uint2 v = *reinterpret_cast<const uint2*>(p);
@@ -275,7 +302,7 @@ template <int BM, int MODE>
 __device__ __forceinline__ void tile(const Prod& a, int block, uint8_t* lds) {
   constexpr bool PKO = MODE == DGU || MODE == DX || MODE == WGRAD, QKO = MODE == WGRAD;
   static_assert(!QKO || BM == 128, "K-outer rows are 128 columns");
-  constexpr int TM = BM / 32, TN = BN / 32, RING = ring<BM>(), STAGE = stage_bytes<BM>(), QOFF = BN * 64;
+  constexpr int TM = BM / 32, TN = BN / 32, RING = ring<BM>(), STAGE = stage_bytes<BM>(), QOFF = BN * 128;
   constexpr int NOUT = MODE == GATE ? BN / 2 : BN;   // output columns of the tile
   // consecutive workgroups run on different XCDs; the m-tiles of one P tile
   // follow each other on one XCD, so its L2 reads the weights once
@@ -284,101 +311,177 @@ __device__ __forceinline__ void tile(const Prod& a, int block, uint8_t* lds) {
   if (unit >= a.ntiles * a.S) return;
   const int nt = unit % a.ntiles, split = unit / a.ntiles;
   const int m0 = mt * BM, n0 = nt * NOUT;
-  const int stages = (a.K + 31) / 32;
+  const int stages = (a.K + 63) / 64;
   const int s0 = (int)((int64_t)split * stages / a.S), n = (int)((int64_t)(split + 1) * stages / a.S) - s0;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int r16 = lane & 15, g4 = lane >> 4;
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave & 1, wn = (wave >> 1) & 1, half = wave >> 2;
   const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
 
   Loader<BN, PKO> lp;
   Loader<BM, QKO> lq;
-  lp.init(a.p, a.ldp, s0, a.N, [&](int r) {
-    if constexpr (PKO) {
-      return n0 + r;
-    } else if constexpr (MODE == GATE) {
-      // a wavefront's 64 rows: 32 gate rows, then the matching up rows
+  if constexpr (PKO) {
+    lp.init(a.p + n0, a.ldp, s0, [&](int c) -> int64_t { return min(c, a.N - 8 - n0); });
+  } else if constexpr (MODE == GATE) {
+    // a wavefront's 64 rows: 32 gate rows, then the matching up rows
+    lp.init(a.p + n0 * a.ldp, a.ldp, s0, [&](int r) -> int64_t {
       const int w = r / (BN / 2), p = r % (BN / 2);
-      return min(n0 + w * (BN / 4) + p % (BN / 4), a.N - 1) + (p < BN / 4 ? 0 : a.N);
-    } else {
-      return min(n0 + r, a.N - 1);
-    }
-  });
-  lq.init(a.q, a.ldq, s0, a.M, [&](int r) { return QKO ? m0 + r : min(m0 + r, a.M - 1); });
+      return min(w * (BN / 4) + p % (BN / 4), a.N - 1 - n0) + (p < BN / 4 ? 0 : a.N);
+    });
+  } else {
+    lp.init(a.p + n0 * a.ldp, a.ldp, s0, [&](int r) -> int64_t { return min(r, a.N - 1 - n0); });
+  }
+  if constexpr (QKO) {
+    lq.init(a.q + m0, a.ldq, s0, [&](int c) -> int64_t { return min(c, a.M - 8 - m0); });
+  } else {
+    lq.init(a.q + m0 * a.ldq, a.ldq, s0, [&](int r) -> int64_t { return min(r, a.M - 1 - m0); });
+  }
   constexpr int LPW = Loader<BN, PKO>::N + Loader<BM, QKO>::N;
-  int issued = 0;   // stages
-  auto issue = [&]() {
-    const uint32_t b = base + (uint32_t)(issued % RING) * STAGE;
-    const int left = a.K - 32 * (s0 + issued);
-    lp.issue(b, left);
-    lq.issue(b + QOFF, left);
-    ++issued;
+  // of this range's stages, those whose 64 k are all there
+  const int whole = min(n, a.K / 64 - s0);
+  auto issue = [&](int s, uint32_t b) {   // stage s into the buffer at b
+    if (s < whole) {
+      lp.issue(b);
+      lq.issue(b + QOFF);
+    } else {
+      const int left = a.K - 64 * (s0 + s);
+      lp.issue_partial(b, left);
+      lq.issue_partial(b + QOFF, left);
+    }
   };
-  // fragment addresses within a stage
+  // fragment addresses within a stage, at this wavefront's half of its K
   uint32_t po[TN], qo[TM];
-  const int slot = (g4 ^ fwd::swz64(r16)) << 4;
+  const int slot = ((4 * half + g4) ^ (r16 & 7)) << 4;
 #pragma unroll
   for (int i = 0; i < TN; ++i) {
     const int r = wn * (BN / 2) + 16 * i;
-    po[i] = PKO ? ko_off(r) : (uint32_t)((r + r16) * 64 + slot);
+    po[i] = PKO ? ko_off(r) + half * 32 * KO_PITCH : (uint32_t)((r + r16) * 128 + slot);
   }
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     const int r = wm * (BM / 2) + 16 * j;
-    qo[j] = QOFF + (QKO ? ko_off(r) : (uint32_t)((r + r16) * 64 + slot));
+    qo[j] = QOFF + (QKO ? ko_off(r) + half * 32 * KO_PITCH : (uint32_t)((r + r16) * 128 + slot));
   }
   f32x4_t acc[TN][TM];
 #pragma unroll
   for (int i = 0; i < TN; ++i)
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < RING - 1 && i < n; ++i) issue();
-  int cur = 0;
-  for (int s = 0; s < n; ++s) {
-    // this wavefront's loads of stage s have landed, its reads of stage s - 1
-    // are done; behind the barrier, everybody's
-    const int later = min(RING - 2, n - 1 - s);
-    __builtin_amdgcn_sched_barrier(0);
-    switch (later) {
-      case 0: MOE_WAIT_VMCNT(0); break;
-      case 1: MOE_WAIT_VMCNT(LPW); break;
-      case 2: MOE_WAIT_VMCNT(2 * LPW); break;
-      case 3: MOE_WAIT_VMCNT(3 * LPW); break;
-      default: MOE_WAIT_VMCNT((RING - 2) * LPW); break;
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-    asm volatile("s_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    if (s + RING - 1 < n) issue();        // into the buffer of stage s - 1
-    const uint8_t* const buf = lds + cur * STAGE;
-    cur = cur + 1 == RING ? 0 : cur + 1;
-    bf16x8_t fp[TN], fq[TM];
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      if constexpr (PKO) {
-        fp[i] = ko_read(buf, po[i]);
-      } else {
-        fp[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4*>(buf + po[i]));
-      }
-    }
+  struct Frags {
+    bf16x8_t p[TN], q[TM];
+  };
+  auto read = [&](Frags& f, int at) {   // the stage in ring position `at`
+    const uint8_t* const buf = lds + at * STAGE;
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       if constexpr (QKO) {
-        fq[j] = ko_read(buf, qo[j]);
+        f.q[j] = ko_read(buf, qo[j]);
       } else {
-        fq[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4*>(buf + qo[j]));
+        f.q[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4*>(buf + qo[j]));
       }
     }
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      if constexpr (PKO) {
+        f.p[i] = ko_read(buf, po[i]);
+      } else {
+        f.p[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4*>(buf + po[i]));
+      }
+    }
+  };
+  auto mma = [&](const Frags& f) {
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[i], fq[j], acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
+  };
+  // All but the last `LATER` stages' loads of this wavefront have landed and
+  // its fragment reads are done; behind the barrier, everybody's.
+  auto sync = [&](auto later) {
+    __builtin_amdgcn_sched_barrier(0);
+    MOE_WAIT_VMCNT(decltype(later)::value * LPW);
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using None = std::integral_constant<int, 0>;
+  using Most = std::integral_constant<int, RING - 2>;
+  if (n > 0) {
+    int issued = 0;
+    for (; issued < RING && issued < n; ++issued) issue(issued, base + issued * STAGE);
+    Frags f, g;
+    if (n >= RING) {
+      sync(std::integral_constant<int, RING - 1>());
+    } else {
+      sync(None());
+    }
+    read(f, 0);
+    // Iteration s: the fragments of stage s are being read.  Once everybody has
+    // them and the loads of stage s + 1 are here, the buffer of stage s takes
+    // stage s + RING, the next fragments are read, and stage s is multiplied.
+    // RING of them at a time while the stages to load are whole: constant
+    // waits, addresses and no branches (a loop with those measured 1900 cycles
+    // a stage, whatever was taken out of it)
+    static_assert(RING % 2 == 0, "the two fragment sets alternate");
+    int s = 0;
+    for (; s + 2 * RING <= whole; s += RING) {
+#pragma unroll
+      for (int u = 0; u < RING; ++u) {
+        sync(Most());
+        lp.issue(base + u * STAGE);
+        lq.issue(base + u * STAGE + QOFF);
+        read(u % 2 ? f : g, (u + 1) % RING);
+        mma(u % 2 ? g : f);
+      }
+    }
+    issued = max(issued, min(n, s + RING));
+    int at = 0;   // ring position of stage s
+    auto iter = [&](const Frags& now, Frags& next) {
+      if (s + 1 < n) {
+        if (issued - s == RING) {
+          sync(Most());
+        } else {
+          sync(None());
+        }
+        if (issued < n) issue(issued++, base + at * STAGE);
+        at = at + 1 == RING ? 0 : at + 1;
+        read(next, at);
+      }
+      mma(now);
+      ++s;
+    };
+    while (s + 2 <= n) {
+      iter(f, g);
+      iter(g, f);
+    }
+    if (s < n) iter(f, g);
+  }
+  // The two halves of K: each keeps half of the rows and adds what the other
+  // half's wavefront sends through LDS.
+  {
+    constexpr int HM = TM / 2;
+    f32x4_t* const box = reinterpret_cast<f32x4_t*>(lds);
+    __syncthreads();   // every wavefront has left the ring
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < HM; ++j)
+        box[((wave * TN + i) * HM + j) * 64 + lane] = half ? acc[i][j] : acc[i][HM + j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < HM; ++j) {
+        // the lower half of K first, whoever adds
+        const f32x4_t o = box[(((wave ^ 4) * TN + i) * HM + j) * 64 + lane];
+        acc[i][j] = half ? o + acc[i][HM + j] : acc[i][j] + o;
+      }
   }
   // lane: row r16 of each 16, four consecutive columns from 4 g4
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int m = m0 + wm * (BM / 2) + j * 16 + r16;
+  for (int j = 0; j < TM / 2; ++j) {
+    const int m = m0 + wm * (BM / 2) + (half * (TM / 2) + j) * 16 + r16;
     if (m >= a.M) continue;
     constexpr int NI = MODE == GATE ? TN / 2 : TN;
 #pragma unroll
@@ -398,8 +501,8 @@ __device__ __forceinline__ void tile(const Prod& a, int block, uint8_t* lds) {
 }
 
 template <int BM, int MODE>
-__global__ __launch_bounds__(256, 2) void tile_kernel(Prod a) {
-  __shared__ __align__(1024) uint8_t lds[ring<BM>() * stage_bytes<BM>()];
+__global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Prod a) {
+  __shared__ __align__(1024) uint8_t lds[tile_lds<BM>()];
   tile<BM, MODE>(a, (int)blockIdx.x, lds);
 }
 
@@ -410,8 +513,8 @@ struct Backward {
   int blocks_dx, blocks_dw1;
 };
 template <int BM>
-__global__ __launch_bounds__(256, 2) void backward_kernel(Backward a) {
-  __shared__ __align__(1024) uint8_t lds[ring<128>() * stage_bytes<128>()];
+__global__ __launch_bounds__(kTileThreads, 2) void backward_kernel(Backward a) {
+  __shared__ __align__(1024) uint8_t lds[std::max(tile_lds<BM>(), tile_lds<128>())];
   int b = (int)blockIdx.x;
   if (b < a.blocks_dx) {
     tile<BM, DX>(a.dx, b, lds);
@@ -465,8 +568,8 @@ Plan choose_form(Mode mode, int64_t M, int N, int K, bool many) {
   if (many && 4 * big >= 3 * (int64_t)cus) return {MANY, 0, 1};
   const int BM = M <= 64 && mode != WGRAD ? 64 : 128;
   const int64_t tiles = std::max<int64_t>(1, (M + BM - 1) / BM) * ((N + nout - 1) / nout);
-  const int stages = (K + 31) / 32;
-  const int S = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, stages / 8), 2 * cus / tiles));
+  const int stages = (K + 63) / 64;
+  const int S = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, stages / 4), cus / tiles));
   return {TILES, BM, S};
 }
 
@@ -493,9 +596,9 @@ moe_status_t run_tiles(Prod a, const Plan& p, hipStream_t s) {
   const int64_t blocks = lay_out((Mode)MODE, a, p);
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (p.BM == 64) {
-    hipLaunchKernelGGL((tile_kernel<64, MODE>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<64, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
   } else {
-    hipLaunchKernelGGL((tile_kernel<128, MODE>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<128, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
   }
   if (status() != MOE_OK) return MOE_ERR_HIP;
   if (p.S > 1) {
@@ -654,9 +757,9 @@ extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const 
     b.blocks_dx = (int)n0;
     b.blocks_dw1 = (int)n1;
     if (p.bm_dx == 64) {
-      hipLaunchKernelGGL((backward_kernel<64>), dim3((unsigned)(n0 + n1 + n2)), dim3(256), 0, s, b);
+      hipLaunchKernelGGL((backward_kernel<64>), dim3((unsigned)(n0 + n1 + n2)), dim3(kTileThreads), 0, s, b);
     } else {
-      hipLaunchKernelGGL((backward_kernel<128>), dim3((unsigned)(n0 + n1 + n2)), dim3(256), 0, s, b);
+      hipLaunchKernelGGL((backward_kernel<128>), dim3((unsigned)(n0 + n1 + n2)), dim3(kTileThreads), 0, s, b);
     }
     return ffn::status();
   }

@@ -543,7 +543,7 @@ moe_status_t moe_add_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const vo
  * Every T >= 0 runs, a single token included (T <= 16 reads the weights once,
  * straight into the matrix instructions' operands).  Results do not depend on
  * thread timing.  Limits: d % 8 == 0, f % 8 == 0, 8 <= d, f <= 2^20,
- * 2 f d < 2^31, T < 2^31; all pointers 16-byte aligned. */
+ * 2 f d < 2^31, T < 2^31, pitches <= 2^23; all pointers 16-byte aligned. */
 size_t moe_gated_ffn_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t keep_h, int32_t strided_x);
 moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, const uint16_t* w2,
                            const uint16_t* res, int64_t ldres, int64_t T, int32_t d, int32_t f, uint16_t* h,

@@ -174,6 +174,7 @@ def test_ffn_refusals(L):
     assert _ffn(L, y=FAKE) == INVALID                                     # onto x
     assert _ffn(L, ldx=56) == INVALID and _ffn(L, res=FAKE, ldr=8) == INVALID
     assert _ffn(L, res=2 * FAKE, ldr=72) == INVALID                       # in place at another pitch
+    assert _ffn(L, ldx=(1 << 23) + 8) == UNSUPPORTED and _ffn(L, res=FAKE, ldr=1 << 24) == UNSUPPORTED
     assert _ffn(L, ldx=65) == ALIGN and _ffn(L, res=FAKE, ldr=68) == ALIGN
     for name in ("x", "w1", "w2", "res", "y"):
         assert _ffn(L, **{"ldr": 64, name: 2 * FAKE + 8}) == ALIGN, name
