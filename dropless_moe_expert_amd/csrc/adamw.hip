@@ -40,23 +40,8 @@ __device__ __forceinline__ int state_exponent(float amax) {
   return max(-127, min(127, ef - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u)));
 }
 
-// a value scaled into [-448, 448], rounded to the E4M3 grid by 16 random
-// bits: the low 20 mantissa bits are cut after the bits were added at their
-// top; below the smallest normal, 2^-6 is added first so that the cut falls
-// on the subnormals' grid of 2^-9
-__device__ __forceinline__ float round_e4m3(float a, uint32_t rnd16) {
-  const float mag = fabsf(a);
-  const bool low = mag < 0.015625f;
-  const float base = low ? mag + 0.015625f : mag;
-  const float cut = __uint_as_float((__float_as_uint(base) + (rnd16 << 4)) & 0xFFF00000u);
-  return copysignf(low ? cut - 0.015625f : cut, a);
-}
-
-__device__ __forceinline__ uint32_t round_bf16(float p, uint32_t rnd16) {
-  const uint32_t u = __float_as_uint(p);
-  if ((u & 0x7F800000u) == 0x7F800000u) return f32_to_bf16_bits(p);
-  return (u + rnd16) >> 16;
-}
+// finite p: 16 random bits added right below bf16's, the rest cut
+__device__ __forceinline__ uint32_t round_bf16(float p, uint32_t rnd16) { return (__float_as_uint(p) + rnd16) >> 16; }
 
 __device__ __forceinline__ void ldf8(const float* p, float* f) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
@@ -67,41 +52,51 @@ __device__ __forceinline__ void stf8(float* p, const float* f) {
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
-// eight E4M3 codes times 2^e
+// eight E4M3 codes times 2^(scale - 127), scale 255: NaN (one scaled
+// conversion a pair; checked on the hardware for every code and scale)
 __device__ __forceinline__ void ld_codes8(uint2 q, uint8_t scale, float* f) {
-  const float s = scale == 255 ? __uint_as_float(0x7FC00000u) : mx_scale_operand((int)scale - 127);
-  const float tiny = scale == 0 ? __uint_as_float(0x00400000u) : s;   // 2^-127 is subnormal
+  const float s = __uint_as_float((uint32_t)scale << 23);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int w = h ? (int)q.y : (int)q.x;
-    f[4 * h + 0] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * tiny;
-    f[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * tiny;
-    f[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * tiny;
-    f[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * tiny;
+    const uint32_t w = h ? q.y : q.x;
+    const f32x2_v lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, false);
+    const f32x2_v hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, true);
+    f[4 * h + 0] = lo[0];
+    f[4 * h + 1] = lo[1];
+    f[4 * h + 2] = hi[0];
+    f[4 * h + 3] = hi[1];
   }
 }
 
 // The codes of eight neighbouring elements of a block whose other elements
-// the three neighbouring lanes hold; returns the scale byte.
-__device__ __forceinline__ uint32_t st_codes8(const float* f, const uint32_t* rnd, int sh, uint2& q) {
+// the three neighbouring lanes hold; returns the scale byte.  The conversion
+// adds the seed's top bits below the kept mantissa bits (of a subnormal code
+// too) and cuts: checked on the hardware against that rule for 4 million
+// values in [-448, 448] with 16 random bits at the top of the seed.
+// HIGH: the element's bits are the high half of rnd, else the low half.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t st_codes8(const float* f, const uint32_t* rnd, uint2& q) {
   float m = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = mx_absmax(m, f[j]);
-  m = mx_absmax(m, __shfl_xor(m, 1, 64));
-  m = mx_absmax(m, __shfl_xor(m, 2, 64));
+  m = mx_absmax(m, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(m), 0xB1, 0xF, 0xF, false)));   // lane ^ 1
+  m = mx_absmax(m, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(m), 0x4E, 0xF, 0xF, false)));   // lane ^ 2
   const int e = state_exponent(m);
   if (e == kMxNaN) {
     q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
     return 255u;
   }
-  float o[8];
+  const float k = e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
+  int w[2] = {0, 0};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = round_e4m3(scale_pow2(f[j], e), (rnd[j] >> sh) & 0xFFFFu);
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[0], o[1], 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[2], o[3], lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[4], o[5], 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[6], o[7], hi, true);
-  q = make_uint2((uint32_t)lo, (uint32_t)hi);
+  for (int h = 0; h < 2; ++h) {
+    auto seed = [&](int j) { return (int)(HIGH ? rnd[4 * h + j] & 0xFFFF0000u : rnd[4 * h + j] << 16); };
+    w[h] = __builtin_amdgcn_cvt_sr_fp8_f32(f[4 * h + 0] * k, seed(0), w[h], 0);
+    w[h] = __builtin_amdgcn_cvt_sr_fp8_f32(f[4 * h + 1] * k, seed(1), w[h], 1);
+    w[h] = __builtin_amdgcn_cvt_sr_fp8_f32(f[4 * h + 2] * k, seed(2), w[h], 2);
+    w[h] = __builtin_amdgcn_cvt_sr_fp8_f32(f[4 * h + 3] * k, seed(3), w[h], 3);
+  }
+  q = make_uint2((uint32_t)w[0], (uint32_t)w[1]);
   return (uint32_t)(e + 127);
 }
 
@@ -206,20 +201,29 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
       if constexpr (S8) v[j] *= v[j];
       m[j] = fmaf(a.b1, m[j], a.omb1 * gj);
       v[j] = fmaf(a.b2, v[j], a.omb2 * gj * gj);
-      sv[j] = sqrtf(v[j]);
+      sv[j] = __builtin_amdgcn_sqrtf(v[j]);   // 1 ulp, as the reciprocal below
       const float upd = (m[j] * ic1) * __builtin_amdgcn_rcpf(fmaf(sv[j], ic2, a.eps));
       p[j] = fmaf(-a.lr, fmaf(a.wd, p[j], upd), p[j]);
     }
     uint2 qm, qv;
     uint32_t em = 0, ev = 0;
     if constexpr (S8) {
-      em = st_codes8(m, rnd, 0, qm);
-      ev = st_codes8(sv, rnd, 16, qv);
+      em = st_codes8<false>(m, rnd, qm);
+      ev = st_codes8<true>(sv, rnd, qv);
     }
     uint32_t pb[8];
     if constexpr (PM == PM_BF16) {
+      float z = 0.f;   // NaN if any value is infinite or NaN: these are not to be cut
 #pragma unroll
-      for (int j = 0; j < 8; ++j) pb[j] = round_bf16(p[j], mix32(rnd[j] + 0x9E3779B9u) & 0xFFFFu);
+      for (int j = 0; j < 8; ++j) {
+        pb[j] = round_bf16(p[j], mix32(rnd[j] + 0x9E3779B9u) & 0xFFFFu);
+        z = fmaf(p[j], 0.f, z);
+      }
+      if (z != 0.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((__float_as_uint(p[j]) & 0x7F800000u) == 0x7F800000u) pb[j] = f32_to_bf16_bits(p[j]);
+      }
     }
     if constexpr (S8) {
       if ((threadIdx.x & 3) == 0 && live > 0) {

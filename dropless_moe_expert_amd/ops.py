@@ -683,19 +683,30 @@ def _need(ok: bool, what: str) -> None:
 
 def _rows(t: torch.Tensor, what: str) -> int:
     """The row pitch of a 2-D GPU tensor whose rows are contiguous."""
-    _need(t.is_cuda and t.dim() == 2, f"{what}: a 2-D tensor on the GPU")
+    if not t.is_cuda or t.dim() != 2:
+        raise MoeError(what + ": a 2-D tensor on the GPU")
     T, d = t.shape
-    st = t.stride()
-    _need(T == 0 or d <= 1 or st[1] == 1, f"{what}: the elements of a row must be contiguous")
-    if T <= 1:
+    if t.is_contiguous():
         return d
-    _need(st[0] >= d, f"{what}: rows must not overlap")
-    return st[0]
+    row, elem = t.stride()
+    if d > 1 and elem != 1:
+        raise MoeError(what + ": the elements of a row must be contiguous")
+    if T > 1 and row < d:
+        raise MoeError(what + ": rows must not overlap")
+    return row if T > 1 else d
 
 
 def _float_code(t: torch.Tensor, what: str) -> int:
-    _need(t.dtype in (torch.bfloat16, torch.float32), f"{what}: bf16 or fp32")
-    return MOE_OUT_F32 if t.dtype == torch.float32 else MOE_OUT_BF16
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return MOE_OUT_BF16
+    if dt is torch.float32:
+        return MOE_OUT_F32
+    raise MoeError(what + ": bf16 or fp32")
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _invoke(dev: torch.device, what: str, *args) -> None:
@@ -703,15 +714,25 @@ def _invoke(dev: torch.device, what: str, *args) -> None:
     current stream as the last argument."""
     fn = getattr(lib(), what)
     if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev)), what)
+        status = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)), what)
+            status = fn(*args, _raw_stream(dev.index))
+    if status:
+        _check(status, what)
+
+
+def _raw_stream(index: int) -> int:
+    """The device's current stream: what torch.cuda.current_stream() returns,
+    without the object around it (2 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _same_device(dev: torch.device, *ts) -> None:
+    i = dev.index
     for t in ts:
-        _need(t is None or t.device == dev, "tensors must be on one GPU")
+        if t is not None and t.get_device() != i:
+            raise MoeError("tensors must be on one GPU")
 
 
 def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
@@ -725,34 +746,35 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     0)), s, rstd fp32 [T] (keep_rstd=True)), None where not asked for.
     out_s: where s goes (residual itself: updated in place)."""
     ldx = _rows(x, "x")
-    _need(x.dtype == torch.bfloat16, "x: bf16")
+    _need(x.dtype is torch.bfloat16, "x: bf16")
     _need(bf16 or mxfp8, "add_rmsnorm: no output asked for")
-    T, d = x.shape
+    T, d = shape = x.shape
     dev = x.device
     _same_device(dev, weight, residual, out_s)
     _need(weight.shape == (d,) and weight.is_contiguous(), "weight: [d], contiguous")
     r_code = ldr = lds = 0
-    s = x
+    s, s_at = x, None
     if residual is not None:
         ldr = _rows(residual, "residual")
-        _need(residual.shape == x.shape, "residual: the shape of x")
+        _need(residual.shape == shape, "residual: the shape of x")
         r_code = _float_code(residual, "residual")
         if out_s is None:
-            s, lds = torch.empty((T, d), dtype=residual.dtype, device=dev), d
+            s, lds = torch.empty(shape, dtype=residual.dtype, device=dev), d
         else:
             lds = _rows(out_s, "out_s")
-            _need(out_s.shape == x.shape and out_s.dtype == residual.dtype, "out_s: shape and type of the residual")
+            _need(out_s.shape == shape and out_s.dtype is residual.dtype, "out_s: shape and type of the residual")
             s = out_s
+        s_at = s.data_ptr()
     else:
         _need(out_s is None, "out_s without a residual: s is x itself")
-    y = torch.empty((T, d), dtype=torch.bfloat16, device=dev) if bf16 else None
+    y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if bf16 else None
     q = sc = None
     if mxfp8:
-        q = torch.empty((T, d), dtype=torch.uint8, device=dev)
+        q = torch.empty(shape, dtype=torch.uint8, device=dev)
         sc = torch.empty((T, d // 32), dtype=torch.uint8, device=dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev) if keep_rstd else None
-    _invoke(dev, "moe_add_rmsnorm", _ptr(x), ldx, _ptr(weight), _float_code(weight, "weight"), _ptr(residual), r_code,
-            ldr, None if residual is None else _ptr(s), lds, T, d, eps, _ptr(y), _ptr(q), _ptr(sc), _ptr(rstd))
+    _invoke(dev, "moe_add_rmsnorm", x.data_ptr(), ldx, weight.data_ptr(), _float_code(weight, "weight"), _addr(residual),
+            r_code, ldr, s_at, lds, T, d, eps, _addr(y), _addr(q), _addr(sc), _addr(rstd))
     return dict(y=y, q=q, scale=sc, s=s, rstd=rstd)
 
 
@@ -780,9 +802,9 @@ def add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
     dw = torch.empty(d, dtype=torch.float32, device=dev)
     need = lib().moe_add_rmsnorm_backward_workspace_bytes(T, d)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _invoke(dev, "moe_add_rmsnorm_backward", _ptr(dy), lddy, _ptr(s), code, lds, _ptr(weight),
-            _float_code(weight, "weight"), _ptr(rstd), _ptr(dresidual), ldr, T, d, _ptr(dx), _ptr(ds), _ptr(dw),
-            _ptr(ws), need)
+    _invoke(dev, "moe_add_rmsnorm_backward", dy.data_ptr(), lddy, s.data_ptr(), code, lds, weight.data_ptr(),
+            _float_code(weight, "weight"), rstd.data_ptr(), _addr(dresidual), ldr, T, d, dx.data_ptr(), _addr(ds),
+            dw.data_ptr(), ws.data_ptr(), need)
     return dict(dx=dx, ds=dx if ds is None else ds, dweight=dw)
 
 
@@ -824,8 +846,8 @@ def gated_ffn(x: torch.Tensor, w1p: torch.Tensor, w2: torch.Tensor, residual: Op
         gu = torch.empty((T, 2 * f), dtype=torch.bfloat16, device=dev)
     need = lib().moe_gated_ffn_workspace_bytes(T, d, f, int(keep), int(ldx != d))
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _invoke(dev, "moe_gated_ffn", _ptr(x), ldx, _ptr(w1p), _ptr(w2), _ptr(residual), ldr, T, d, f, _ptr(h), _ptr(gu),
-            _ptr(out), _ptr(ws), need)
+    _invoke(dev, "moe_gated_ffn", x.data_ptr(), ldx, w1p.data_ptr(), w2.data_ptr(), _addr(residual), ldr, T, d, f,
+            _addr(h), _addr(gu), out.data_ptr(), ws.data_ptr(), need)
     return (out, dict(h=h, gu=gu)) if keep else out
 
 
@@ -849,9 +871,9 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, saved: dict, w1p: torc
     dw2 = torch.empty((d, f), dtype=out_dtype, device=dev)
     need = lib().moe_gated_ffn_backward_workspace_bytes(T, d, f)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _invoke(dev, "moe_gated_ffn_backward", _ptr(dy), _ptr(x), _ptr(saved["gu"]), _ptr(saved["h"]), _ptr(w1p), _ptr(w2),
-            T, d, f, MOE_OUT_F32 if out_dtype == torch.float32 else MOE_OUT_BF16, _ptr(dgu), _ptr(dx), _ptr(dw1p),
-            _ptr(dw2), _ptr(ws), need)
+    _invoke(dev, "moe_gated_ffn_backward", *[t.data_ptr() for t in (dy, x, saved["gu"], saved["h"], w1p, w2)], T, d, f,
+            MOE_OUT_F32 if out_dtype == torch.float32 else MOE_OUT_BF16,
+            *[t.data_ptr() for t in (dgu, dx, dw1p, dw2, ws)], need)
     return dict(dx=dx, dw1p=dw1p, dw2=dw2, dgu=dgu)
 
 
@@ -897,6 +919,7 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step: torch.Tensor, *, lr: fl
     n = len(params)
     _need(step.is_cuda and step.dtype == torch.int32 and step.numel() == 1, "step: int32 [1] on the GPU")
     dev = step.device
+    index = dev.index
     if grad_scale is not None:
         _need(grad_scale.device == dev and grad_scale.dtype == torch.float32 and grad_scale.numel() == 1,
               "grad_scale: fp32 [1] on the GPU")
@@ -920,11 +943,12 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step: torch.Tensor, *, lr: fl
         if ts is None:
             table[k::8] = [0] * n
             continue
-        _need(len(ts) == n, f"{what}: one tensor for each of params")
-        for i, t in enumerate(ts):
-            want = numels[i] if k < 5 else (numels[i] + 31) // 32
-            if t.dtype not in types or t.numel() != want or t.device != dev or not t.is_contiguous():
-                raise MoeError(f"{what}[{i}]: contiguous, on the GPU of step, of the type and size that go with params[{i}]")
+        if len(ts) != n:
+            raise MoeError(what + ": one tensor for each of params")
+        want = numels if k < 5 else [(m + 31) // 32 for m in numels]
+        if [t.numel() for t in ts] != want or not all([t.dtype in types and t.get_device() == index and t.is_contiguous()
+                                                       for t in ts]):
+            raise MoeError(what + ": contiguous, on the GPU of step, of the types and sizes that go with params")
         ptrs = [t.data_ptr() for t in ts]
         table[k::8] = ptrs
         if k != 2:
@@ -933,7 +957,7 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step: torch.Tensor, *, lr: fl
     c = AdamwConfig(lr, betas[0], betas[1], eps, weight_decay, 8 if bits8 else 32,
                     MOE_OUT_F32 if pt == torch.float32 else MOE_OUT_BF16,
                     MOE_OUT_F32 if gt == torch.float32 else MOE_OUT_BF16, seed & 0xFFFFFFFF)
-    _invoke(dev, "moe_adamw_step", (ctypes.c_int64 * (8 * n))(*table), n, ctypes.byref(c), _ptr(step), _ptr(grad_scale))
+    _invoke(dev, "moe_adamw_step", (ctypes.c_int64 * (8 * n))(*table), n, ctypes.byref(c), step.data_ptr(), _addr(grad_scale))
 
 
 # ------------------------------------------------------------------ measurement only

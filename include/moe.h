@@ -571,7 +571,7 @@ moe_status_t moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, const
  * moe_pack_weights and the quantisers read the result).  With t = *step + 1:
  *   g = grad * grad_scale;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
  *   p = p - lr (wd p + (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
- * in fp32.  `tensors` is a HOST array of `count` entries, read during the
+ * in fp32 (a v below fp32's normal range has the root 0).  `tensors` is a HOST array of `count` entries, read during the
  * call; the addresses in it are device pointers and travel as kernel
  * arguments, so the call may be captured.
  *   param    bf16 or fp32 (param_dtype) [n]
