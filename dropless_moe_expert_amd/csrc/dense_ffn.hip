@@ -558,19 +558,58 @@ struct Plan {
   int BM, S;
 };
 
+// What the forms cost, in microseconds, from times measured on MI355X; only
+// their order matters.  A stage of a 128 x 128 tile (64 deep) takes 0.57 with K
+// contiguous (T = 1024, d = 7168, f = 2048: 1 x 112 + 2 x 32 stages in 116 us),
+// 0.80 with one K-outer operand (T = 4096: 2 x 112 in 180), 0.85 with two; of a
+// 64-row tile about 3/4 of that, as its loads.  A launch, with a tile's first
+// loads and its stores, takes 5; the weights cannot come faster than 4.5 TB/s;
+// joining splits moves their partial sums out and in at about 4 TB/s behind a
+// launch of 4.  A stage (32 deep) of the 256 x 256 kernels takes 0.9, a launch 8.
+double stage_us(Mode mode, int BM) {
+  const double t = mode == GATE || mode == DOWN ? 0.57 : mode == WGRAD ? 0.85 : 0.80;
+  return BM == 64 ? 0.75 * t : t;
+}
+double join_us(Mode mode, int64_t M, int N, int S) {
+  return S > 1 ? 4 + 8.0 * S * (double)M * (mode == GATE ? 2 * N : N) / 4e6 : 0;
+}
+int64_t tiles_of(Mode mode, int64_t M, int N, int BM) {
+  const int nout = mode == GATE ? BN / 2 : BN;
+  return std::max<int64_t>(1, (M + BM - 1) / BM) * ((N + nout - 1) / nout);
+}
+double many_us(Mode mode, int64_t M, int N, int K) {
+  const int nout = mode == GATE ? BN / 2 : BN, cus = moe_host::device_cu_count();
+  const int64_t tiles = std::max<int64_t>(1, (M + 255) / 256) * ((N + 2 * nout - 1) / (2 * nout));
+  return 8 + (double)((tiles + cus - 1) / cus) * ((K + 31) / 32) * 0.9;
+}
+
 // How a product of M rows, N output columns (GATE: N pairs) and contraction K
 // runs.  `many`: whether the 256 x 256 kernels take its shapes.
 Plan choose_form(Mode mode, int64_t M, int N, int K, bool many) {
-  const int cus = moe_host::device_cu_count();
-  const int nout = mode == GATE ? BN / 2 : BN;
-  if (M <= 16 && (mode == GATE || mode == DOWN)) return {FEW, 0, 1};
-  const int64_t big = ((M + 255) / 256) * ((N + 2 * nout - 1) / (2 * nout));
-  if (many && 4 * big >= 3 * (int64_t)cus) return {MANY, 0, 1};
-  const int BM = M <= 64 && mode != WGRAD ? 64 : 128;
-  const int64_t tiles = std::max<int64_t>(1, (M + BM - 1) / BM) * ((N + nout - 1) / nout);
+  const int64_t cus = moe_host::device_cu_count();
+  const int64_t weights = (int64_t)(mode == GATE ? 2 * N : N) * K;
+  // Few tokens: with up to 16 the wavefronts' token loads cost as many L2
+  // requests as the weights', so with more than four the largest weights go
+  // faster through the tiles (d = 4096, f = 14336: 8 tokens 87 against 77 us;
+  // d = 7168, f = 2048: 16 tokens 28 both; d = 2048, f = 768: 14 against 19)
+  if ((mode == GATE || mode == DOWN) && M <= 16 && (M <= 4 || weights <= (1 << 25))) return {FEW, 0, 1};
+  Plan best{TILES, 128, 1};
+  double least = 1e300;
   const int stages = (K + 63) / 64;
-  const int S = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, stages / 4), cus / tiles));
-  return {TILES, BM, S};
+  for (int BM = 64; BM <= 128; BM += 64) {
+    if (BM == 64 && M > 64) continue;
+    for (int S = 1; S <= 16 && (S == 1 || stages / S >= 4); ++S) {
+      const int64_t rounds = (tiles_of(mode, M, N, BM) * S + cus - 1) / cus;
+      const double us = 5 + std::max((double)rounds * ((stages + S - 1) / S) * stage_us(mode, BM), 2.0 * weights / 4.5e6) +
+                        join_us(mode, M, N, S);
+      if (us < least) {
+        least = us;
+        best = {TILES, BM, S};
+      }
+    }
+  }
+  if (many && many_us(mode, M, N, K) < least) return {MANY, 0, 1};
+  return best;
 }
 
 size_t part_bytes(Mode mode, const Plan& p, int64_t M, int N) {
@@ -592,6 +631,14 @@ int64_t lay_out(Mode mode, Prod& a, const Plan& p) {
 }
 
 template <int MODE>
+moe_status_t run_join(const Prod& a, hipStream_t s) {
+  const int64_t total = (int64_t)a.M * (a.N / 4);
+  const int64_t blocks = std::min<int64_t>((total + 255) / 256, 16 * (int64_t)moe_host::device_cu_count());
+  hipLaunchKernelGGL((join_kernel<MODE>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  return status();
+}
+
+template <int MODE>
 moe_status_t run_tiles(Prod a, const Plan& p, hipStream_t s) {
   const int64_t blocks = lay_out((Mode)MODE, a, p);
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
@@ -601,12 +648,7 @@ moe_status_t run_tiles(Prod a, const Plan& p, hipStream_t s) {
     hipLaunchKernelGGL((tile_kernel<128, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
   }
   if (status() != MOE_OK) return MOE_ERR_HIP;
-  if (p.S > 1) {
-    const int64_t total = (int64_t)a.M * (a.N / 4);
-    const int64_t nb = std::min<int64_t>((total + 255) / 256, 16 * (int64_t)moe_host::device_cu_count());
-    hipLaunchKernelGGL((join_kernel<MODE>), dim3((unsigned)nb), dim3(256), 0, s, a);
-  }
-  return status();
+  return p.S > 1 ? run_join<MODE>(a, s) : MOE_OK;
 }
 
 Prod product(const uint16_t* p, int64_t ldp, const uint16_t* q, int64_t ldq, void* out, int64_t M, int N, int K,
@@ -642,18 +684,39 @@ GGArgs one_group(const void* A, const void* B, void* C, void* aux, int64_t T, in
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// the backward's first product, and whether the others (dx, dw1p, dw2) run
-// as the one launch of tiles
+// The backward: its first product, and the three that follow it (dx, dw1p,
+// dw2).  Those of the three that are no better off in the 256 x 256 kernels
+// share one launch of tiles; where one of them has few, long tiles its K is
+// split, so that none outlasts the chip's share of the whole.
 struct BackwardPlan {
-  Plan dgu;
-  bool tiles;
-  int bm_dx;
+  Plan dgu, rest[3];
+};
+struct Shape {
+  Mode mode;
+  int64_t M;
+  int N, K;
 };
 BackwardPlan plan_backward(int64_t T, int d, int f) {
   const int64_t cus = moe_host::device_cu_count();
-  const bool many = d % 64 == 0 && f % 32 == 0;
-  const int64_t m = (T + 255) / 256, big = m * ((d + 255) / 256);
-  return {choose_form(DGU, T, f, d, many), !many || 4 * big < 3 * cus, T <= 64 ? 64 : 128};
+  const bool many = d % 64 == 0 && f % 32 == 0 && T > 0;
+  BackwardPlan p{choose_form(DGU, T, f, d, many), {}};
+  const Shape sh[3] = {{DX, T, d, 2 * f}, {WGRAD, 2 * f, d, (int)T}, {WGRAD, d, f, (int)T}};
+  double work = 0;   // of the shared launch, us on the whole chip
+  double one[3];     // one unsplit tile, us
+  for (int i = 0; i < 3; ++i) {
+    const int BM = sh[i].mode == DX && T <= 64 ? 64 : 128;
+    one[i] = ((sh[i].K + 63) / 64) * stage_us(sh[i].mode, BM);
+    const double us = (double)tiles_of(sh[i].mode, sh[i].M, sh[i].N, BM) * one[i] / cus;
+    p.rest[i] = many && many_us(sh[i].mode, sh[i].M, sh[i].N, sh[i].K) < us ? Plan{MANY, 0, 1} : Plan{TILES, BM, 1};
+    if (p.rest[i].form == TILES) work += us;
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (p.rest[i].form != TILES) continue;
+    const int most = std::min(16, std::max(1, (sh[i].K + 63) / 64 / 4));
+    const int S = std::min(most, (int)std::min(16.0, one[i] / std::max(work, 3.0) + 1));
+    if (S > 1 && join_us(sh[i].mode, sh[i].M, sh[i].N, S) < one[i] - std::max(work, one[i] / S)) p.rest[i].S = S;
+  }
+  return p;
 }
 
 }  // namespace ffn
@@ -714,20 +777,34 @@ extern "C" moe_status_t moe_gated_ffn_launch(const uint16_t* x, int64_t ldx, con
   return launch_fwd(g, MOE_EPI_NONE, 0, MOE_B_NK, s);
 }
 
+// Workspace of the backward: the row count, then the partial sums: the first
+// product's and the split tail's share the place that the others' follow.
 extern "C" size_t moe_gated_ffn_backward_ws_impl(int64_t T, int32_t d, int32_t f) {
   const BackwardPlan p = plan_backward(T, d, f);
-  return 256 + std::max(part_bytes(DGU, p.dgu, T, f), p.tiles ? (size_t)0 : fwd_split_workspace_bytes());
+  size_t first = part_bytes(DGU, p.dgu, T, f), rest = 0;
+  if (p.rest[0].form == MANY) {
+    first = std::max(first, fwd_split_workspace_bytes());
+  } else {
+    rest += up256(part_bytes(DX, p.rest[0], T, d));
+  }
+  if (p.rest[1].form == TILES) rest += up256(part_bytes(WGRAD, p.rest[1], 2 * (int64_t)f, d));
+  if (p.rest[2].form == TILES) rest += up256(part_bytes(WGRAD, p.rest[2], d, f));
+  return 256 + up256(first) + rest;
 }
 
 extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const uint16_t* x, const uint16_t* gu,
                                                       const uint16_t* h, const uint16_t* w1p, const uint16_t* w2,
                                                       int64_t T, int32_t d, int32_t f, uint16_t* dgu, uint16_t* dx,
                                                       void* dw1p, void* dw2, int out_f32, void* ws, hipStream_t s) {
-  int32_t* const rows = reinterpret_cast<int32_t*>(ws);
-  float* const part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + 256);
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  int32_t* const rows = reinterpret_cast<int32_t*>(w);
+  float* const part = reinterpret_cast<float*>(w + 256);
   const BackwardPlan p = plan_backward(T, d, f);
+  size_t first = part_bytes(DGU, p.dgu, T, f);
+  if (p.rest[0].form == MANY) first = std::max(first, fwd_split_workspace_bytes());
+  w += 256 + up256(first);
   moe_status_t st = MOE_OK;
-  if (p.dgu.form == MANY || !p.tiles) {
+  if (p.dgu.form == MANY || p.rest[0].form == MANY || p.rest[1].form == MANY || p.rest[2].form == MANY) {
     hipLaunchKernelGGL(set_rows_kernel, dim3(1), dim3(1), 0, s, rows, (int32_t)T);
     st = ffn::status();
     if (st != MOE_OK) return st;
@@ -744,35 +821,50 @@ extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const 
     }
     if (st != MOE_OK) return st;
   }
-  // dx = dgu W1p, dW1p = dgu^T x, dW2 = dy^T h
-  if (p.tiles) {
-    Backward b;
-    b.dx = product(w1p, d, dgu, 2 * (int64_t)f, dx, T, d, 2 * f, nullptr);
-    b.dw1 = product(x, d, dgu, 2 * (int64_t)f, dw1p, 2 * f, d, (int)T, nullptr);
-    b.dw2 = product(h, f, dy, d, dw2, d, f, (int)T, nullptr);
-    b.dw1.out_f32 = b.dw2.out_f32 = out_f32;
-    const int64_t n0 = T > 0 ? lay_out(DX, b.dx, {TILES, p.bm_dx, 1}) : 0;
-    const int64_t n1 = lay_out(WGRAD, b.dw1, {TILES, 128, 1}), n2 = lay_out(WGRAD, b.dw2, {TILES, 128, 1});
-    if (n0 + n1 + n2 > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-    b.blocks_dx = (int)n0;
-    b.blocks_dw1 = (int)n1;
-    if (p.bm_dx == 64) {
-      hipLaunchKernelGGL((backward_kernel<64>), dim3((unsigned)(n0 + n1 + n2)), dim3(kTileThreads), 0, s, b);
-    } else {
-      hipLaunchKernelGGL((backward_kernel<128>), dim3((unsigned)(n0 + n1 + n2)), dim3(kTileThreads), 0, s, b);
-    }
-    return ffn::status();
+  // dx = dgu W1p, dW1p = dgu^T x, dW2 = dy^T h: first those of the 256 x 256 kernels
+  if (p.rest[0].form == MANY && T > 0) {
+    st = launch_fwd(one_group(dgu, w1p, dx, nullptr, T, d, 2 * f, rows, part), MOE_EPI_NONE, 0, MOE_B_KN, s);
+    if (st != MOE_OK) return st;
   }
-  st = launch_fwd(one_group(dgu, w1p, dx, nullptr, T, d, 2 * f, rows, part), MOE_EPI_NONE, 0, MOE_B_KN, s);
-  if (st == MOE_OK) {
+  if (p.rest[1].form == MANY) {
     GGArgs g = one_group(dgu, x, dw1p, nullptr, T, d, 0, rows, nullptr);
     g.M = 2 * f;
     st = launch_wgrad(g, out_f32, s);
+    if (st != MOE_OK) return st;
   }
-  if (st == MOE_OK) {
+  if (p.rest[2].form == MANY) {
     GGArgs g = one_group(dy, h, dw2, nullptr, T, f, 0, rows, nullptr);
     g.M = d;
     st = launch_wgrad(g, out_f32, s);
+    if (st != MOE_OK) return st;
   }
+  Backward b;
+  b.dx = product(w1p, d, dgu, 2 * (int64_t)f, dx, T, d, 2 * f, nullptr);
+  b.dw1 = product(x, d, dgu, 2 * (int64_t)f, dw1p, 2 * (int64_t)f, d, (int)T, nullptr);
+  b.dw2 = product(h, f, dy, d, dw2, d, f, (int)T, nullptr);
+  b.dw1.out_f32 = b.dw2.out_f32 = out_f32;
+  Prod* const prod[3] = {&b.dx, &b.dw1, &b.dw2};
+  const Mode mode[3] = {DX, WGRAD, WGRAD};
+  int64_t blocks[3] = {0, 0, 0};
+  for (int i = 0; i < 3; ++i) {
+    if (p.rest[i].form != TILES || (i == 0 && T == 0)) continue;
+    prod[i]->part = reinterpret_cast<float*>(w);
+    w += up256(part_bytes(mode[i], p.rest[i], prod[i]->M, prod[i]->N));
+    blocks[i] = lay_out(mode[i], *prod[i], p.rest[i]);
+  }
+  const int64_t all = blocks[0] + blocks[1] + blocks[2];
+  if (all == 0) return MOE_OK;
+  if (all > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  b.blocks_dx = (int)blocks[0];
+  b.blocks_dw1 = (int)blocks[1];
+  if (p.rest[0].form == TILES && p.rest[0].BM == 64) {
+    hipLaunchKernelGGL((backward_kernel<64>), dim3((unsigned)all), dim3(kTileThreads), 0, s, b);
+  } else {
+    hipLaunchKernelGGL((backward_kernel<128>), dim3((unsigned)all), dim3(kTileThreads), 0, s, b);
+  }
+  if (ffn::status() != MOE_OK) return MOE_ERR_HIP;
+  if (blocks[0] && b.dx.S > 1) st = run_join<DX>(b.dx, s);
+  if (st == MOE_OK && blocks[1] && b.dw1.S > 1) st = run_join<WGRAD>(b.dw1, s);
+  if (st == MOE_OK && blocks[2] && b.dw2.S > 1) st = run_join<WGRAD>(b.dw2, s);
   return st;
 }
