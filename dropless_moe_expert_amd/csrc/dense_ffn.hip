@@ -558,20 +558,21 @@ struct Plan {
   int BM, S;
 };
 
-// What the forms cost, in microseconds, from times measured on MI355X; only
-// their order matters.  A stage of a 128 x 128 tile (64 deep) takes 0.57 with K
-// contiguous (T = 1024, d = 7168, f = 2048: 1 x 112 + 2 x 32 stages in 116 us),
-// 0.80 with one K-outer operand (T = 4096: 2 x 112 in 180), 0.85 with two; of a
-// 64-row tile about 3/4 of that, as its loads.  A launch, with a tile's first
-// loads and its stores, takes 5; the weights cannot come faster than 4.5 TB/s;
-// joining splits moves their partial sums out and in at about 4 TB/s behind a
-// launch of 4.  A stage (32 deep) of the 256 x 256 kernels takes 0.9, a launch 8.
+// What the forms cost, in microseconds; only their order matters.  Constants
+// fitted to 102 sizes (three of the products, 17 to 4096 tokens, widths 768 to
+// 14336, every tile height and split) timed on MI355X: the choice they lead to
+// is 0.7 % from the best one on average, 8 % at most.  A stage (64 deep) of a
+// 128 x 128 tile takes 0.60 with K contiguous, 0.78 with a K-outer operand
+// (two: 0.85, from the backward's second launch), of a 64 x 128 tile 0.67 of
+// that; down to 0.68 of it where the tiles do not fill the chip.  A launch, its
+// first loads and its stores, 5; joining splits 3.1 and their partial sums out
+// and in at 5 TB/s.  A stage (32 deep) of the 256 x 256 kernels 0.84, a launch 4.
 double stage_us(Mode mode, int BM) {
-  const double t = mode == GATE || mode == DOWN ? 0.57 : mode == WGRAD ? 0.85 : 0.80;
-  return BM == 64 ? 0.75 * t : t;
+  const double t = mode == GATE || mode == DOWN ? 0.60 : mode == WGRAD ? 0.85 : 0.78;
+  return BM == 64 ? 0.67 * t : t;
 }
 double join_us(Mode mode, int64_t M, int N, int S) {
-  return S > 1 ? 4 + 8.0 * S * (double)M * (mode == GATE ? 2 * N : N) / 4e6 : 0;
+  return S > 1 ? 3.1 + 8.0 * S * (double)M * (mode == GATE ? 2 * N : N) / 5e6 : 0;
 }
 int64_t tiles_of(Mode mode, int64_t M, int N, int BM) {
   const int nout = mode == GATE ? BN / 2 : BN;
@@ -580,7 +581,7 @@ int64_t tiles_of(Mode mode, int64_t M, int N, int BM) {
 double many_us(Mode mode, int64_t M, int N, int K) {
   const int nout = mode == GATE ? BN / 2 : BN, cus = moe_host::device_cu_count();
   const int64_t tiles = std::max<int64_t>(1, (M + 255) / 256) * ((N + 2 * nout - 1) / (2 * nout));
-  return 8 + (double)((tiles + cus - 1) / cus) * ((K + 31) / 32) * 0.9;
+  return 4 + (double)((tiles + cus - 1) / cus) * ((K + 31) / 32) * 0.84;
 }
 
 // How a product of M rows, N output columns (GATE: N pairs) and contraction K
@@ -597,11 +598,11 @@ Plan choose_form(Mode mode, int64_t M, int N, int K, bool many) {
   double least = 1e300;
   const int stages = (K + 63) / 64;
   for (int BM = 64; BM <= 128; BM += 64) {
-    if (BM == 64 && M > 64) continue;
-    for (int S = 1; S <= 16 && (S == 1 || stages / S >= 4); ++S) {
-      const int64_t rounds = (tiles_of(mode, M, N, BM) * S + cus - 1) / cus;
-      const double us = 5 + std::max((double)rounds * ((stages + S - 1) / S) * stage_us(mode, BM), 2.0 * weights / 4.5e6) +
-                        join_us(mode, M, N, S);
+    for (int S = 1; S <= 16 && (S == 1 || stages / S >= 2); ++S) {
+      const int64_t tiles = tiles_of(mode, M, N, BM) * S, rounds = (tiles + cus - 1) / cus;
+      const double fill = rounds > 1 ? 1.0 : 0.68 + 0.32 * (double)tiles / (double)cus;
+      const double us =
+          5 + (double)rounds * ((stages + S - 1) / S) * stage_us(mode, BM) * fill + join_us(mode, M, N, S);
       if (us < least) {
         least = us;
         best = {TILES, BM, S};
@@ -705,9 +706,14 @@ BackwardPlan plan_backward(int64_t T, int d, int f) {
   double one[3];     // one unsplit tile, us
   for (int i = 0; i < 3; ++i) {
     const int BM = sh[i].mode == DX && T <= 64 ? 64 : 128;
-    one[i] = ((sh[i].K + 63) / 64) * stage_us(sh[i].mode, BM);
+    // A tile's first loads and stores take 1.7 us; a 256 x 256 weight gradient's
+    // 8, and 16 once (d = 7168, f = 2048: dw2, one round, 256 tokens 29 us, 4096
+    // tokens 112; the three of 256 tokens 151 there, 97 as tiles of one launch)
+    one[i] = ((sh[i].K + 63) / 64) * stage_us(sh[i].mode, BM) + 1.7;
     const double us = (double)tiles_of(sh[i].mode, sh[i].M, sh[i].N, BM) * one[i] / cus;
-    p.rest[i] = many && many_us(sh[i].mode, sh[i].M, sh[i].N, sh[i].K) < us ? Plan{MANY, 0, 1} : Plan{TILES, BM, 1};
+    const int64_t rounds = ((sh[i].M + 255) / 256 * ((sh[i].N + 255) / 256) + cus - 1) / cus;
+    const double large = 16 + (double)rounds * (((sh[i].K + 31) / 32) * 0.80 + 8);
+    p.rest[i] = many && large < us ? Plan{MANY, 0, 1} : Plan{TILES, BM, 1};
     if (p.rest[i].form == TILES) work += us;
   }
   for (int i = 0; i < 3; ++i) {
