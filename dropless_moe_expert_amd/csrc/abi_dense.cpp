@@ -12,7 +12,7 @@
 #include "moe.h"
 
 extern "C" {
-int moe_norm_backward_parts(int64_t);
+int moe_norm_backward_parts(int64_t, int32_t);
 moe_status_t moe_add_rmsnorm_launch(const moe::NormArgs*, int, int, hipStream_t);
 moe_status_t moe_rmsnorm_backward_launch(const moe::NormBwdArgs*, int, int, float*, hipStream_t);
 size_t moe_gated_ffn_ws_impl(int64_t, int32_t, int32_t, int, int);
@@ -90,7 +90,7 @@ moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ldx, const void* w, int3
 
 size_t moe_add_rmsnorm_backward_workspace_bytes(int64_t T, int32_t d) {
   if (T < 0 || T > INT32_MAX || d < 1 || d > kNormMaxD) return 0;
-  const size_t n = (size_t)moe_norm_backward_parts(T) * (size_t)d * 4;
+  const size_t n = (size_t)moe_norm_backward_parts(T, d) * (size_t)d * 4;
   return n < 256 ? 256 : n;
 }
 

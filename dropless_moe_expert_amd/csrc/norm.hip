@@ -9,43 +9,97 @@
 // differentiates what the forward computed.  Backward, with xh = s * rstd:
 //   ds = dres + rstd * (w * dy - xh * mean(w * dy * xh)),  dw = sum_rows dy * xh
 //
-// Bound: HBM.  A row is read once into registers by TPR threads (one
-// wavefront, 256 or 1024 threads), its sum of squares taken there and its
-// outputs written from there; the weight comes from L2.  All arithmetic and
-// every sum is fp32.
+// Bound: HBM.  A row is read once into registers by TPR threads (8 to 64 of a
+// wavefront, or 256 or 1024), its sum of squares taken there and its outputs
+// written from there; the weight comes from L2.  All arithmetic and every sum
+// is fp32.  Rows move in 16-byte pieces whatever their alignment (gfx950 loads
+// and stores them from any element's address); a row whose d is no multiple
+// of 8 ends in a piece of single elements.
+#include <type_traits>
+
 #include "common.h"
 #include "dense_args.h"
 
 namespace moe {
 
-__device__ __forceinline__ void load8_f32(const float* p, float* f) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));   // 16 bytes at any bf16
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));      // and at any fp32
+
+// Piece v (elements 8v .. 8v + 7) of a row of d.  ANY: unaligned, and the last
+// piece may be in part (its missing elements read as 0 and are not written).
+template <bool ANY>
+__device__ __forceinline__ uint4 load_piece(const uint16_t* row, int v, int d) {
+  if constexpr (!ANY) return reinterpret_cast<const uint4*>(row)[v];
+  if (8 * v + 8 <= d) {
+    const u32x4_any u = *reinterpret_cast<const u32x4_any*>(row + 8 * v);
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 7; ++j)
+    if (8 * v + j < d) w[j >> 1] |= (uint32_t)row[8 * v + j] << (16 * (j & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8_f32(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+template <bool ANY>
+__device__ __forceinline__ void store_piece(uint16_t* row, int v, int d, uint4 o) {
+  if constexpr (!ANY) {
+    reinterpret_cast<uint4*>(row)[v] = o;
+    return;
+  }
+  if (8 * v + 8 <= d) {
+    *reinterpret_cast<u32x4_any*>(row + 8 * v) = u32x4_any{o.x, o.y, o.z, o.w};
+    return;
+  }
+  const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+  for (int j = 0; j < 7; ++j)
+    if (8 * v + j < d) row[8 * v + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+}
+template <bool ANY>
+__device__ __forceinline__ void load_piece(const float* row, int v, int d, float* f) {
+  using V = std::conditional_t<ANY, f32x4_any, f32x4_t>;
+  if (!ANY || 8 * v + 8 <= d) {
+    const V a = reinterpret_cast<const V*>(row + 8 * v)[0], b = reinterpret_cast<const V*>(row + 8 * v)[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = a[j];
+      f[4 + j] = b[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 8 * v + j < d ? row[8 * v + j] : 0.f;
+  }
+}
+template <bool ANY>
+__device__ __forceinline__ void store_piece(float* row, int v, int d, const float* f) {
+  using V = std::conditional_t<ANY, f32x4_any, f32x4_t>;
+  if (!ANY || 8 * v + 8 <= d) {
+    reinterpret_cast<V*>(row + 8 * v)[0] = V{f[0], f[1], f[2], f[3]};
+    reinterpret_cast<V*>(row + 8 * v)[1] = V{f[4], f[5], f[6], f[7]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (8 * v + j < d) row[8 * v + j] = f[j];
+  }
 }
 
 // weight elements 8v .. 8v + 7
-__device__ __forceinline__ void load_w8(const void* w, int w_f32, int v, float* f) {
+template <bool ANY>
+__device__ __forceinline__ void load_weight(const void* w, int w_f32, int v, int d, float* f) {
   if (w_f32) {
-    load8_f32(reinterpret_cast<const float*>(w) + 8 * v, f);
+    load_piece<ANY>(reinterpret_cast<const float*>(w), v, d, f);
   } else {
-    unpack8(reinterpret_cast<const uint4*>(w)[v], f);
+    unpack8(load_piece<ANY>(reinterpret_cast<const uint16_t*>(w), v, d), f);
   }
 }
-__device__ __forceinline__ float load_w1(const void* w, int w_f32, int e) {
-  return w_f32 ? reinterpret_cast<const float*>(w)[e] : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(w)[e]);
-}
 
-// Sum of v over the TPR threads of a row (one wavefront, or the workgroup
-// through one LDS word per wavefront: `slot` picks one of two such sets, so
-// that two sums in a row need one barrier each).
+// Sum of v over the TPR threads of a row (lanes of one wavefront, or the
+// workgroup through one LDS word per wavefront: `slot` picks one of two such
+// sets, so that two sums in a row need one barrier each).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, int slot) {
-  v = wave_sum(v);
+#pragma unroll
+  for (int o = (TPR < kWave ? TPR : kWave) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
   if constexpr (TPR > kWave) {
     constexpr int NW = TPR / kWave;
     __shared__ float part[2][NW];
@@ -73,40 +127,39 @@ struct Row8<RES_F32> {
   }
 };
 
-// 16-byte path: d % 8 == 0, rows and pointers 16-byte aligned.  Thread t of a
-// row holds the 8-element pieces t, t + TPR, ...; the four lanes of an MXFP8
-// block are neighbours.
-template <int TPR, int VPT, int RT>
+// Thread t of a row holds the 8-element pieces t, t + TPR, ...; the four lanes
+// of an MXFP8 block are neighbours.
+template <int TPR, int VPT, int RT, bool ANY>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(NormArgs a) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
-  if (row >= a.T) return;   // RPW > 1: a whole wavefront, and row_sum has no barrier
-  const int nvec = a.d / 8;
-  const uint4* xr = reinterpret_cast<const uint4*>(a.x + row * a.ldx);
+  if (row >= a.T) return;   // RPW > 1: all threads of a row, whose sum has no barrier then
+  const int nvec = (a.d + 7) / 8;
+  const uint16_t* xr = a.x + row * a.ldx;
   Row8<RT> sv[VPT];
   float sq = 0.f;
   if constexpr (RT == RES_NONE) {
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = t + TPR * k;
-      sv[k].b = v < nvec ? xr[v] : make_uint4(0, 0, 0, 0);
+      sv[k].b = v < nvec ? load_piece<ANY>(xr, v, a.d) : make_uint4(0, 0, 0, 0);
     }
   } else {
     uint4 xv[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = t + TPR * k;
-      xv[k] = v < nvec ? xr[v] : make_uint4(0, 0, 0, 0);
+      xv[k] = v < nvec ? load_piece<ANY>(xr, v, a.d) : make_uint4(0, 0, 0, 0);
     }
     if constexpr (RT == RES_BF16) {
-      const uint4* rr = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.r) + row * a.ldr);
+      const uint16_t* rr = reinterpret_cast<const uint16_t*>(a.r) + row * a.ldr;
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int v = t + TPR * k;
-        sv[k].b = v < nvec ? rr[v] : make_uint4(0, 0, 0, 0);
+        sv[k].b = v < nvec ? load_piece<ANY>(rr, v, a.d) : make_uint4(0, 0, 0, 0);
       }
-      uint4* sr = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.s) + row * a.lds);
+      uint16_t* sr = reinterpret_cast<uint16_t*>(a.s) + row * a.lds;
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int v = t + TPR * k;
@@ -116,7 +169,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] += g[j];
         sv[k].b = pack8(f);
-        if (v < nvec) sr[v] = sv[k].b;
+        if (v < nvec) store_piece<ANY>(sr, v, a.d, sv[k].b);
       }
     } else {
       const float* rr = reinterpret_cast<const float*>(a.r) + row * a.ldr;
@@ -125,7 +178,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
         const int v = t + TPR * k;
 #pragma unroll
         for (int j = 0; j < 8; ++j) sv[k].v[j] = 0.f;
-        if (v < nvec) load8_f32(rr + 8 * v, sv[k].v);
+        if (v < nvec) load_piece<ANY>(rr, v, a.d, sv[k].v);
       }
       float* sr = reinterpret_cast<float*>(a.s) + row * a.lds;
 #pragma unroll
@@ -135,7 +188,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
         unpack8(xv[k], f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sv[k].v[j] += f[j];
-        if (v < nvec) store8_f32(sr + 8 * v, sv[k].v);
+        if (v < nvec) store_piece<ANY>(sr, v, a.d, sv[k].v);
       }
     }
   }
@@ -154,12 +207,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
     if (v >= nvec) continue;   // the four lanes of a block stay together: nvec % 4 == 0 where codes are written
     float f[8], w[8];
     sv[k].get(f);
-    load_w8(a.w, a.w_f32, v, w);
+    load_weight<ANY>(a.w, a.w_f32, v, a.d, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
     const uint4 o = pack8(f);
-    if (a.y) reinterpret_cast<uint4*>(a.y + row * a.d)[v] = o;
-    if (a.q) {
+    if (a.y) store_piece<ANY>(a.y + row * a.d, v, a.d, o);
+    if (!ANY && a.q) {
       uint32_t m = max_u16x2(max_u16x2(mag_pair(o.x), mag_pair(o.y)), max_u16x2(mag_pair(o.z), mag_pair(o.w)));
       m = max_u16x2(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, false));   // lane ^ 1
       m = max_u16x2(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, false));   // lane ^ 2
@@ -178,63 +231,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
   }
 }
 
-// Any d and alignment, bf16 output: thread t holds the elements t, t + TPR, ...
-// (neighbouring lanes read neighbouring elements).
-template <int TPR, int EPT, int RT>
-__global__ __launch_bounds__(TPR) void add_rmsnorm_any_kernel(NormArgs a) {
-  const int t = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  const uint16_t* xr = a.x + row * a.ldx;
-  float s[EPT];
-#pragma unroll
-  for (int k = 0; k < EPT; ++k) {
-    const int e = t + TPR * k;
-    s[k] = e < a.d ? bf16_bits_to_f32(xr[e]) : 0.f;
-  }
-  if constexpr (RT == RES_BF16) {
-    const uint16_t* rr = reinterpret_cast<const uint16_t*>(a.r) + row * a.ldr;
-    uint16_t* sr = reinterpret_cast<uint16_t*>(a.s) + row * a.lds;
-#pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      const int e = t + TPR * k;
-      if (e < a.d) {
-        const uint32_t b = f32_to_bf16_bits(s[k] + bf16_bits_to_f32(rr[e]));
-        sr[e] = (uint16_t)b;
-        s[k] = bf16_bits_to_f32(b);
-      }
-    }
-  } else if constexpr (RT == RES_F32) {
-    const float* rr = reinterpret_cast<const float*>(a.r) + row * a.ldr;
-    float* sr = reinterpret_cast<float*>(a.s) + row * a.lds;
-#pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      const int e = t + TPR * k;
-      if (e < a.d) sr[e] = s[k] += rr[e];
-    }
-  }
-  float sq = 0.f;
-#pragma unroll
-  for (int k = 0; k < EPT; ++k) sq = fmaf(s[k], s[k], sq);
-  const float rstd = 1.0f / sqrtf(row_sum<TPR>(sq, 0) / (float)a.d + a.eps);
-  if (a.rstd && t == 0) a.rstd[row] = rstd;
-#pragma unroll
-  for (int k = 0; k < EPT; ++k) {
-    const int e = t + TPR * k;
-    if (e < a.d) a.y[row * a.d + e] = (uint16_t)f32_to_bf16_bits(s[k] * rstd * load_w1(a.w, a.w_f32, e));
-  }
-}
-
 // ------------------------------------------------------------------ backward
 
 // Each workgroup walks rows blockIdx, blockIdx + grid, ... (RPW at a time)
 // and keeps its share of dw in registers; the next row's loads are in flight
 // while a row is reduced and written.  The workgroups' sums go to part and
 // are added by norm_dw_kernel in a fixed order: no atomics.
-template <int TPR, int VPT, int ST>
+template <int TPR, int VPT, int ST, bool ANY>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel(NormBwdArgs a) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const int nvec = a.d / 8;
+  const int nvec = (a.d + 7) / 8;
   struct In {
     uint4 dy[VPT];
     Row8<ST> s[VPT], dr[VPT];
@@ -246,7 +253,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
     const int v = t + TPR * k;
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[k][j] = acc[k][j] = 0.f;
-    if (v < nvec) load_w8(a.w, a.w_f32, v, w[k]);
+    if (v < nvec) load_weight<ANY>(a.w, a.w_f32, v, a.d, w[k]);
   }
   auto load_s = [&](const void* p, int64_t ld, int64_t row, Row8<ST> (&o)[VPT]) {
 #pragma unroll
@@ -255,9 +262,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
       if constexpr (ST == RES_F32) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[k].v[j] = 0.f;
-        if (v < nvec) load8_f32(reinterpret_cast<const float*>(p) + row * ld + 8 * v, o[k].v);
+        if (v < nvec) load_piece<ANY>(reinterpret_cast<const float*>(p) + row * ld, v, a.d, o[k].v);
       } else {
-        o[k].b = v < nvec ? reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + row * ld)[v]
+        o[k].b = v < nvec ? load_piece<ANY>(reinterpret_cast<const uint16_t*>(p) + row * ld, v, a.d)
                           : make_uint4(0, 0, 0, 0);
       }
     }
@@ -267,7 +274,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = t + TPR * k;
-      in.dy[k] = v < nvec ? reinterpret_cast<const uint4*>(a.dy + row * a.lddy)[v] : make_uint4(0, 0, 0, 0);
+      in.dy[k] = v < nvec ? load_piece<ANY>(a.dy + row * a.lddy, v, a.d) : make_uint4(0, 0, 0, 0);
     }
     load_s(a.s, a.lds, row, in.s);
     if (a.dres) load_s(a.dres, a.lddres, row, in.dr);
@@ -305,9 +312,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
         for (int j = 0; j < 8; ++j) o[j] += dr[j];
       }
       if constexpr (ST == RES_F32) {
-        store8_f32(a.ds + row * a.d + 8 * v, o);
+        store_piece<ANY>(a.ds + row * a.d, v, a.d, o);
       }
-      reinterpret_cast<uint4*>(a.dx + row * a.d)[v] = pack8(o);
+      store_piece<ANY>(a.dx + row * a.d, v, a.d, pack8(o));
     }
   };
   int64_t row = (int64_t)blockIdx.x * RPW + sub;
@@ -332,7 +339,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = t + TPR * k;
-      if (v < nvec) store8_f32(out + 8 * v, acc[k]);
+      if (v < nvec) store_piece<ANY>(out, v, a.d, acc[k]);
     }
   } else {
     // the wavefronts' sums meet in LDS
@@ -348,54 +355,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel
       for (int i = 0; i < RPW; ++i) v += sum[i][e];
       out[e] = v;
     }
-  }
-}
-
-// any d and alignment
-template <int TPR, int EPT, int ST>
-__global__ __launch_bounds__(TPR) void rmsnorm_backward_any_kernel(NormBwdArgs a) {
-  const int t = threadIdx.x;
-  float acc[EPT];
-#pragma unroll
-  for (int k = 0; k < EPT; ++k) acc[k] = 0.f;
-  auto load_s = [&](const void* p, int64_t at) {
-    return ST == RES_F32 ? reinterpret_cast<const float*>(p)[at]
-                         : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p)[at]);
-  };
-  int slot = 0;
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-    const float rstd = a.rstd[row];
-    float dy[EPT], xh[EPT], dot = 0.f;
-#pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      const int e = t + TPR * k;
-      dy[k] = e < a.d ? bf16_bits_to_f32(a.dy[row * a.lddy + e]) : 0.f;
-      xh[k] = e < a.d ? load_s(a.s, row * a.lds + e) : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      const int e = t + TPR * k;
-      xh[k] *= rstd;
-      acc[k] = fmaf(dy[k], xh[k], acc[k]);
-      dy[k] = e < a.d ? dy[k] * load_w1(a.w, a.w_f32, e) : 0.f;
-      dot = fmaf(dy[k], xh[k], dot);
-    }
-    const float c = row_sum<TPR>(dot, slot) / (float)a.d;
-    slot ^= 1;
-#pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      const int e = t + TPR * k;
-      if (e >= a.d) continue;
-      float o = rstd * (dy[k] - xh[k] * c);
-      if (a.dres) o += load_s(a.dres, row * a.lddres + e);
-      if constexpr (ST == RES_F32) a.ds[row * a.d + e] = o;
-      a.dx[row * a.d + e] = (uint16_t)f32_to_bf16_bits(o);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < EPT; ++k) {
-    const int e = t + TPR * k;
-    if (e < a.d) a.part[(int64_t)blockIdx.x * a.d + e] = acc[k];
   }
 }
 
@@ -422,110 +381,101 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__
 
 namespace {
 
-constexpr int kNormParts = 512;   // partial rows of dw at most (two workgroups per compute unit)
-
 moe_status_t status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
-template <int RT>
-void launch_norm(const NormArgs& a, bool vec, hipStream_t s) {
+template <int RT, bool ANY>
+void launch_norm(const NormArgs& a, hipStream_t s) {
   auto go = [&](auto kern, int tpr) {
     const int rpw = tpr < 256 ? 256 / tpr : 1;
     hipLaunchKernelGGL(kern, dim3((unsigned)((a.T + rpw - 1) / rpw)), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
   };
-  if (!vec) {
-    if (a.d <= 1024) {
-      go(add_rmsnorm_any_kernel<256, 4, RT>, 256);
-    } else if (a.d <= 8192) {
-      go(add_rmsnorm_any_kernel<256, 32, RT>, 256);
-    } else {
-      go(add_rmsnorm_any_kernel<1024, 32, RT>, 1024);
-    }
-    return;
-  }
-  const int nvec = a.d / 8;
+  const int nvec = (a.d + 7) / 8;
   // few rows: many threads each, for the latency; many rows: a wavefront each
+  // as far as its registers hold the row
   const bool few = a.T <= 4 * (int64_t)moe_host::device_cu_count();
-  if (nvec <= 64) {
-    go(add_rmsnorm_kernel<64, 1, RT>, 64);
-  } else if (few) {
-    if (nvec <= 256) {
-      go(add_rmsnorm_kernel<256, 1, RT>, 256);
-    } else if (nvec <= 1024) {
-      go(add_rmsnorm_kernel<1024, 1, RT>, 1024);
-    } else {
-      go(add_rmsnorm_kernel<1024, 4, RT>, 1024);
-    }
+  if (nvec <= 8) {
+    go(add_rmsnorm_kernel<8, 1, RT, ANY>, 8);
+  } else if (nvec <= 16) {
+    go(add_rmsnorm_kernel<16, 1, RT, ANY>, 16);
+  } else if (nvec <= 32) {
+    go(add_rmsnorm_kernel<32, 1, RT, ANY>, 32);
+  } else if (nvec <= 64) {
+    go(add_rmsnorm_kernel<64, 1, RT, ANY>, 64);
+  } else if (few && nvec <= 256) {
+    go(add_rmsnorm_kernel<256, 1, RT, ANY>, 256);
+  } else if (few && nvec <= 1024) {
+    go(add_rmsnorm_kernel<1024, 1, RT, ANY>, 1024);
   } else if (nvec <= 128) {
-    go(add_rmsnorm_kernel<64, 2, RT>, 64);
+    go(add_rmsnorm_kernel<64, 2, RT, ANY>, 64);
   } else if (nvec <= 256) {
-    go(add_rmsnorm_kernel<64, 4, RT>, 64);
+    go(add_rmsnorm_kernel<64, 4, RT, ANY>, 64);
   } else if (nvec <= 512) {
-    go(add_rmsnorm_kernel<256, 2, RT>, 256);
+    go(add_rmsnorm_kernel<256, 2, RT, ANY>, 256);
   } else if (nvec <= 1024) {
-    go(add_rmsnorm_kernel<256, 4, RT>, 256);
+    go(add_rmsnorm_kernel<256, 4, RT, ANY>, 256);
   } else {
-    go(add_rmsnorm_kernel<1024, 4, RT>, 1024);
+    go(add_rmsnorm_kernel<1024, 4, RT, ANY>, 1024);
   }
 }
 
-template <int ST>
-void launch_norm_backward(const NormBwdArgs& a, bool vec, int parts, hipStream_t s) {
+template <int ST, bool ANY>
+void launch_norm_backward(const NormBwdArgs& a, int parts, hipStream_t s) {
   auto go = [&](auto kern, int tpr) {
     hipLaunchKernelGGL(kern, dim3((unsigned)parts), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
   };
-  const int nvec = a.d / 8;
-  if (!vec) {
-    if (a.d <= 1024) {
-      go(rmsnorm_backward_any_kernel<256, 4, ST>, 256);
-    } else if (a.d <= 8192) {
-      go(rmsnorm_backward_any_kernel<256, 32, ST>, 256);
-    } else {
-      go(rmsnorm_backward_any_kernel<1024, 32, ST>, 1024);
-    }
+  const int nvec = (a.d + 7) / 8;
+  if (nvec <= 8) {
+    go(rmsnorm_backward_kernel<8, 1, ST, ANY>, 8);
+  } else if (nvec <= 16) {
+    go(rmsnorm_backward_kernel<16, 1, ST, ANY>, 16);
+  } else if (nvec <= 32) {
+    go(rmsnorm_backward_kernel<32, 1, ST, ANY>, 32);
   } else if (nvec <= 64) {
-    go(rmsnorm_backward_kernel<64, 1, ST>, 64);
+    go(rmsnorm_backward_kernel<64, 1, ST, ANY>, 64);
+  } else if (nvec <= 128) {
+    go(rmsnorm_backward_kernel<64, 2, ST, ANY>, 64);
   } else if (nvec <= 256) {
-    go(rmsnorm_backward_kernel<256, 1, ST>, 256);
+    go(rmsnorm_backward_kernel<256, 1, ST, ANY>, 256);
   } else if (nvec <= 512) {
-    go(rmsnorm_backward_kernel<256, 2, ST>, 256);
+    go(rmsnorm_backward_kernel<256, 2, ST, ANY>, 256);
   } else if (nvec <= 1024) {
-    go(rmsnorm_backward_kernel<256, 4, ST>, 256);
+    go(rmsnorm_backward_kernel<256, 4, ST, ANY>, 256);
   } else {
-    go(rmsnorm_backward_kernel<1024, 4, ST>, 1024);
+    go(rmsnorm_backward_kernel<1024, 4, ST, ANY>, 1024);
   }
 }
 
 }  // namespace
 }  // namespace moe
 
-// Workgroups of the backward: every one holds at least one row
-extern "C" int moe_norm_backward_parts(int64_t T) {
-  return (int)std::min<int64_t>(T, moe::kNormParts);
-}
+// Workgroups of the backward, each with a row of column sums: two a compute
+// unit, more where rows are short (a sum of them is then short too)
+extern "C" int moe_norm_backward_parts(int64_t T, int32_t d) { return (int)std::min<int64_t>(T, d <= 256 ? 2048 : 512); }
 
 extern "C" moe_status_t moe_add_rmsnorm_launch(const moe::NormArgs* a, int res, int vec, hipStream_t s) {
-  if (res == moe::RES_NONE) {
-    moe::launch_norm<moe::RES_NONE>(*a, vec, s);
-  } else if (res == moe::RES_BF16) {
-    moe::launch_norm<moe::RES_BF16>(*a, vec, s);
+  using namespace moe;
+  if (res == RES_NONE) {
+    vec ? launch_norm<RES_NONE, false>(*a, s) : launch_norm<RES_NONE, true>(*a, s);
+  } else if (res == RES_BF16) {
+    vec ? launch_norm<RES_BF16, false>(*a, s) : launch_norm<RES_BF16, true>(*a, s);
   } else {
-    moe::launch_norm<moe::RES_F32>(*a, vec, s);
+    vec ? launch_norm<RES_F32, false>(*a, s) : launch_norm<RES_F32, true>(*a, s);
   }
-  return moe::status();
+  return status();
 }
 
 extern "C" moe_status_t moe_rmsnorm_backward_launch(const moe::NormBwdArgs* a, int s_f32, int vec, float* dw,
                                                     hipStream_t s) {
-  const int parts = moe_norm_backward_parts(a->T);
+  using namespace moe;
+  const int parts = moe_norm_backward_parts(a->T, a->d);
   if (parts > 0) {
     if (s_f32) {
-      moe::launch_norm_backward<moe::RES_F32>(*a, vec, parts, s);
+      vec ? launch_norm_backward<RES_F32, false>(*a, parts, s) : launch_norm_backward<RES_F32, true>(*a, parts, s);
     } else {
-      moe::launch_norm_backward<moe::RES_BF16>(*a, vec, parts, s);
+      vec ? launch_norm_backward<RES_BF16, false>(*a, parts, s) : launch_norm_backward<RES_BF16, true>(*a, parts, s);
     }
-    if (moe::status() != MOE_OK) return MOE_ERR_HIP;
+    if (status() != MOE_OK) return MOE_ERR_HIP;
   }
-  hipLaunchKernelGGL(moe::norm_dw_kernel, dim3((unsigned)((a->d + 31) / 32)), dim3(1024), 0, s, a->part, parts, a->d,
-                     dw);
-  return moe::status();
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((a->d + 31) / 32)), dim3(1024), 0, s, a->part, parts, a->d, dw);
+  return status();
 }

@@ -503,9 +503,9 @@ moe_status_t moe_swiglu_backward_mxfp8(const uint16_t* gu, const uint16_t* dh, i
  *   whether or not y is; y and q may not both be NULL;
  *   rstd fp32 [T] or NULL (the backward reads it).
  * Limits: 1 <= d <= 32768 (with q: d % 32 == 0), pitches >= d, T < 2^31.
- * With d % 8 == 0 and 16-byte aligned rows a row moves in 16-byte pieces; any
- * other d, pitch or (2-byte, fp32: 4-byte) alignment is taken too, slower;
- * q needs the former (else MOE_ERR_ALIGNMENT). */
+ * Any d, pitch and alignment to the type is taken; q needs d % 8 == 0 and rows
+ * and weight 16-byte aligned (else MOE_ERR_ALIGNMENT), which are also the
+ * fastest. */
 moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ldx, const void* w, int32_t w_dtype, const void* r,
                              int32_t r_dtype, int64_t ldr, void* s, int64_t lds, int64_t T, int32_t d, float eps,
                              uint16_t* y, uint8_t* q, uint8_t* q_scale, float* rstd, void* stream);

@@ -26,7 +26,7 @@ static std::vector<uint32_t> g_chunks;
 static int g_advanced = 0;
 
 extern "C" {
-int moe_norm_backward_parts(int64_t T) { return (int)(T < 512 ? T : 512); }
+int moe_norm_backward_parts(int64_t T, int32_t) { return (int)(T < 512 ? T : 512); }
 moe_status_t moe_add_rmsnorm_launch(const moe::NormArgs*, int, int, hipStream_t) { ++g_launches; return MOE_OK; }
 moe_status_t moe_rmsnorm_backward_launch(const moe::NormBwdArgs*, int, int, float*, hipStream_t) {
   ++g_launches;

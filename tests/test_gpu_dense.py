@@ -155,8 +155,8 @@ def _check_norm_bwd(ops, dy, s, w, rstd, dres):
     else:
         assert o["ds"] is o["dx"]
     _within(o["dx"], ds, b * (1 + ULP16) + ULP16 * np.abs(ds) + 2.0 ** -133, "dx")
-    # columns: rows of one workgroup in turn, then up to 4 + 16 + 32 partial sums
-    n = -(-T // min(T, 512)) + 60 if T else 0
+    # columns: the rows of one of at least min(T, 512) workgroups in turn, then up to 32 + 64 + 32 partial sums
+    n = -(-T // min(T, 512)) + 130 if T else 0
     _within(o["dweight"], dw, n * ULP32 * np.abs(D * xh).sum(0), "dweight")
     return o
 
