@@ -8,6 +8,7 @@ built library (or without a GPU) every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -705,6 +706,12 @@ def _float_code(t: torch.Tensor, what: str) -> int:
     raise MoeError(what + ": bf16 or fp32")
 
 
+def _like(t: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """A new contiguous tensor of t's shape (torch.empty without its parsing of
+    shape and device)."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -759,7 +766,7 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
         _need(residual.shape == shape, "residual: the shape of x")
         r_code = _float_code(residual, "residual")
         if out_s is None:
-            s, lds = torch.empty(shape, dtype=residual.dtype, device=dev), d
+            s, lds = _like(residual), d
         else:
             lds = _rows(out_s, "out_s")
             _need(out_s.shape == shape and out_s.dtype is residual.dtype, "out_s: shape and type of the residual")
@@ -767,10 +774,10 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
         s_at = s.data_ptr()
     else:
         _need(out_s is None, "out_s without a residual: s is x itself")
-    y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if bf16 else None
+    y = _like(x) if bf16 else None
     q = sc = None
     if mxfp8:
-        q = torch.empty(shape, dtype=torch.uint8, device=dev)
+        q = _like(x, torch.uint8)
         sc = torch.empty((T, d // 32), dtype=torch.uint8, device=dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev) if keep_rstd else None
     _invoke(dev, "moe_add_rmsnorm", x.data_ptr(), ldx, weight.data_ptr(), _float_code(weight, "weight"), _addr(residual),
@@ -797,8 +804,8 @@ def add_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
         ldr = _rows(dresidual, "dresidual")
         _need(dresidual.shape == s.shape and dresidual.dtype == s.dtype, "dresidual: shape and type of s")
     code = _float_code(s, "s")
-    dx = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-    ds = torch.empty((T, d), dtype=torch.float32, device=dev) if code == MOE_OUT_F32 else None
+    dx = _like(dy)
+    ds = _like(s) if code == MOE_OUT_F32 else None
     dw = torch.empty(d, dtype=torch.float32, device=dev)
     need = lib().moe_add_rmsnorm_backward_workspace_bytes(T, d)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
@@ -836,7 +843,7 @@ def gated_ffn(x: torch.Tensor, w1p: torch.Tensor, w2: torch.Tensor, residual: Op
         ldr = _rows(residual, "residual")
         _need(residual.dtype == torch.bfloat16 and residual.shape == x.shape, "residual: bf16, the shape of x")
     if out is None:
-        out = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+        out = _like(x)
     else:
         _same_device(dev, out)
         _need(out.shape == (T, d) and out.dtype == torch.bfloat16 and out.is_contiguous(), "out: bf16 [T, d], contiguous")
@@ -865,10 +872,7 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, saved: dict, w1p: torc
     _need(x.shape == (T, d) and saved["gu"].shape == (T, 2 * f) and saved["h"].shape == (T, f),
           "x: [T, d], gu: [T, 2f], h: [T, f]")
     _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype: bf16 or fp32")
-    dgu = torch.empty((T, 2 * f), dtype=torch.bfloat16, device=dev)
-    dx = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-    dw1p = torch.empty((2 * f, d), dtype=out_dtype, device=dev)
-    dw2 = torch.empty((d, f), dtype=out_dtype, device=dev)
+    dgu, dx, dw1p, dw2 = _like(saved["gu"]), _like(x), _like(w1p, out_dtype), _like(w2, out_dtype)
     need = lib().moe_gated_ffn_backward_workspace_bytes(T, d, f)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     _invoke(dev, "moe_gated_ffn_backward", *[t.data_ptr() for t in (dy, x, saved["gu"], saved["h"], w1p, w2)], T, d, f,
@@ -957,7 +961,9 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step: torch.Tensor, *, lr: fl
     c = AdamwConfig(lr, betas[0], betas[1], eps, weight_decay, 8 if bits8 else 32,
                     MOE_OUT_F32 if pt == torch.float32 else MOE_OUT_BF16,
                     MOE_OUT_F32 if gt == torch.float32 else MOE_OUT_BF16, seed & 0xFFFFFFFF)
-    _invoke(dev, "moe_adamw_step", (ctypes.c_int64 * (8 * n))(*table), n, ctypes.byref(c), step.data_ptr(), _addr(grad_scale))
+    entries = array.array("q", table)   # read during the call
+    _invoke(dev, "moe_adamw_step", entries.buffer_info()[0] if n else None, n, ctypes.byref(c), step.data_ptr(),
+            _addr(grad_scale))
 
 
 # ------------------------------------------------------------------ measurement only
