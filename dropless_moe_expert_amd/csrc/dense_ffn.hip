@@ -11,9 +11,9 @@
 //    workgroup owns 16 weight rows, its wavefronts split K and go straight
 //    from HBM to MFMA fragments, no LDS stage; the wavefronts' sums meet in
 //    LDS in a fixed order;
-//  * a moderate number: 64 or 128 x 128 tiles streamed through LDS, K split
-//    over workgroups until the chip is full, the fp32 partial sums added by a
-//    second kernel in split order;
+//  * a moderate number: 64, 128 or 256 x 128 tiles streamed through LDS, K
+//    split over workgroups until the chip is full, the fp32 partial sums added
+//    by a second kernel in split order;
 //  * many: the persistent 256 x 256 kernels of the grouped products
 //    (gg_bf16.hip) with one group.
 #include <algorithm>
@@ -148,20 +148,24 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(Prod a) {
 }
 
 // ------------------------------------------------------------------ tiles
-// One BM x 128 tile (m x n) of a product, over one range of K.  K is staged
+// One BM x 128 tile (m x n; BM 64, 128 or 256) of a product, over one range of K.  K is staged
 // 64 at a time in a ring of LDS buffers (nearly all of LDS) filled by
-// direct-to-LDS loads, RING stages ahead: the weights stream from
-// HBM, and what is in flight bounds their rate.  64 deep, because a stage's row
-// piece is then a whole 128-byte line: with 32 deep stages the L2 served twice
-// the requests and the weights came at half the rate.  Eight wavefronts, 2 (m)
-// x 2 (n) x 2 halves of every stage's K, so that a wavefront's tile is 64 x 64
-// and reads the fewest LDS bytes an MFMA; the halves' sums meet in LDS at the
-// end.  The fragments of the next stage are read while the present one is
-// multiplied.  An operand with K contiguous is 128-byte rows, 16-byte slots
-// swizzled by row; a K-outer one is 64 rows of 256 bytes whose fragments come
-// through the LDS transpose read (gg_pipeline.h has both layouts at the widths
-// of the 256 x 256 kernels).  Pieces past K are loaded from a page of zeros,
-// rows past M or N repeat the last one and are not stored.
+// direct-to-LDS loads, RING stages ahead.  Bound: what the L2s deliver to the
+// compute units.  With the MFMAs or the fragment reads left out the loop takes
+// as long (T = 1024, d = 7168, f = 2048: 118 us whole, 114 without MFMAs, 69
+// without loads: 14 TB/s), so a 128 x 128 tile reaches 0.94 PFLOP/s and a 256 x
+// 128 one, with 3/4 of the bytes an MFMA, 1.1.  Stages are 64 deep because a
+// row's piece is then a whole 128-byte line: 32 deep, the L2 served twice the
+// requests and the tiles of 181 tokens took 31 us instead of 24.  Eight
+// wavefronts, 2 (m) x 2 (n) x 2 halves of every stage's K, so that a
+// wavefront's tile is BM/2 x 64 and reads the fewest LDS bytes an MFMA; the
+// halves' sums meet in LDS at the end.  The fragments of the next stage are read
+// while the present one is multiplied.  An operand with K contiguous is 128-byte
+// rows, 16-byte slots swizzled by row; a K-outer one is 64 rows of 256 bytes
+// whose fragments come through the LDS transpose read (gg_pipeline.h has both
+// layouts at the widths of the 256 x 256 kernels); neither has bank conflicts.
+// Pieces past K are loaded from a page of zeros, rows past M or N repeat the
+// last one and are not stored.
 constexpr int BN = 128;
 constexpr int KO_PITCH = 256;   // bytes of a K-outer row (128 columns)
 
@@ -247,7 +251,7 @@ __device__ __forceinline__ bf16x8_t ko_read(const uint8_t* buf, uint32_t off) {
 }
 
 template <int BM>
-constexpr int ring() { return BM == 128 ? 4 : 6; }   // 128 or 144 KB: one workgroup a compute unit
+constexpr int ring() { return BM == 256 ? 3 : BM == 128 ? 4 : 6; }   // 128 or 144 KB: one workgroup a compute unit
 template <int BM>
 constexpr int stage_bytes() { return (BM + BN) * 128; }
 template <int BM>
@@ -420,17 +424,17 @@ __device__ __forceinline__ void tile(const Prod& a, int block, uint8_t* lds) {
     // Iteration s: the fragments of stage s are being read.  Once everybody has
     // them and the loads of stage s + 1 are here, the buffer of stage s takes
     // stage s + RING, the next fragments are read, and stage s is multiplied.
-    // RING of them at a time while the stages to load are whole: constant
-    // waits, addresses and no branches (a loop with those measured 1900 cycles
-    // a stage, whatever was taken out of it)
-    static_assert(RING % 2 == 0, "the two fragment sets alternate");
+    // U of them at a time while the stages to load are whole: constant waits,
+    // addresses and no branches (a loop with those measured 1900 cycles a
+    // stage, whatever was taken out of it)
+    constexpr int U = RING % 2 ? 2 * RING : RING;   // the two fragment sets alternate
     int s = 0;
-    for (; s + 2 * RING <= whole; s += RING) {
+    for (; s + U + RING <= whole; s += U) {
 #pragma unroll
-      for (int u = 0; u < RING; ++u) {
+      for (int u = 0; u < U; ++u) {
         sync(Most());
-        lp.issue(base + u * STAGE);
-        lq.issue(base + u * STAGE + QOFF);
+        lp.issue(base + (u % RING) * STAGE);
+        lq.issue(base + (u % RING) * STAGE + QOFF);
         read(u % 2 ? f : g, (u + 1) % RING);
         mma(u % 2 ? g : f);
       }
@@ -563,13 +567,14 @@ struct Plan {
 // 14336, every tile height and split) timed on MI355X: the choice they lead to
 // is 0.7 % from the best one on average, 8 % at most.  A stage (64 deep) of a
 // 128 x 128 tile takes 0.60 with K contiguous, 0.78 with a K-outer operand
-// (two: 0.85, from the backward's second launch), of a 64 x 128 tile 0.67 of
-// that; down to 0.68 of it where the tiles do not fill the chip.  A launch, its
-// first loads and its stores, 5; joining splits 3.1 and their partial sums out
-// and in at 5 TB/s.  A stage (32 deep) of the 256 x 256 kernels 0.84, a launch 4.
+// (two: 0.85, from the backward's second launch), of a 64 or 256 x 128 tile 0.67
+// or 1.72 of that; down to 0.68 of it where the tiles do not fill the chip.  A
+// launch, its first loads and its stores, 5, with 256 rows 6; joining splits 3.1
+// and their partial sums out and in at 5 TB/s.  A stage (32 deep) of the 256 x
+// 256 kernels 0.84, a launch 4.
 double stage_us(Mode mode, int BM) {
   const double t = mode == GATE || mode == DOWN ? 0.60 : mode == WGRAD ? 0.85 : 0.78;
-  return BM == 64 ? 0.67 * t : t;
+  return BM == 64 ? 0.67 * t : BM == 256 ? 1.72 * t : t;
 }
 double join_us(Mode mode, int64_t M, int N, int S) {
   return S > 1 ? 3.1 + 8.0 * S * (double)M * (mode == GATE ? 2 * N : N) / 5e6 : 0;
@@ -597,12 +602,12 @@ Plan choose_form(Mode mode, int64_t M, int N, int K, bool many) {
   Plan best{TILES, 128, 1};
   double least = 1e300;
   const int stages = (K + 63) / 64;
-  for (int BM = 64; BM <= 128; BM += 64) {
+  for (int BM = 64; BM <= 256; BM *= 2) {
     for (int S = 1; S <= 16 && (S == 1 || stages / S >= 2); ++S) {
       const int64_t tiles = tiles_of(mode, M, N, BM) * S, rounds = (tiles + cus - 1) / cus;
       const double fill = rounds > 1 ? 1.0 : 0.68 + 0.32 * (double)tiles / (double)cus;
       const double us =
-          5 + (double)rounds * ((stages + S - 1) / S) * stage_us(mode, BM) * fill + join_us(mode, M, N, S);
+          (BM == 256 ? 6 : 5) + (double)rounds * ((stages + S - 1) / S) * stage_us(mode, BM) * fill + join_us(mode, M, N, S);
       if (us < least) {
         least = us;
         best = {TILES, BM, S};
@@ -645,6 +650,8 @@ moe_status_t run_tiles(Prod a, const Plan& p, hipStream_t s) {
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (p.BM == 64) {
     hipLaunchKernelGGL((tile_kernel<64, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
+  } else if (p.BM == 256) {
+    hipLaunchKernelGGL((tile_kernel<256, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
   } else {
     hipLaunchKernelGGL((tile_kernel<128, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
   }

@@ -225,7 +225,8 @@ def _check_ffn(ops, x, w1, w2, res):
 
 FFN_SIZES = [(1, 8, 8), (1, 64, 8), (1, 512, 256), (2, 72, 40), (15, 264, 136), (16, 1024, 96), (17, 8, 8), (17, 72, 40),
              (33, 520, 264), (63, 200, 72), (64, 128, 64), (65, 1032, 200), (100, 2048, 768), (129, 136, 1032),
-             (200, 264, 72), (255, 64, 64), (300, 4096, 64), (1000, 256, 520), (6200, 640, 1024), (4200, 3008, 64)]
+             (200, 264, 72), (255, 64, 64), (300, 4096, 64), (1000, 256, 520), (6200, 640, 1024), (4200, 3008, 64), (8, 2048, 8704),
+             (5, 4104, 4096), (1500, 2056, 1032)]
 
 
 @pytest.mark.parametrize("T,d,f", FFN_SIZES)
@@ -297,7 +298,7 @@ def _check_ffn_bwd(ops, dy, x, saved, w1, w2, out_dtype):
 @pytest.mark.parametrize("T,d,f", [(1, 64, 32), (1, 128, 64), (2, 64, 96), (33, 128, 160), (255, 320, 64), (257, 64, 288),
                                    (300, 1024, 256), (1000, 256, 768), (1100, 2112, 64),
                                    (1, 8, 8), (3, 72, 40), (65, 200, 136), (130, 1032, 24), (31, 8, 264), (6200, 2112, 64),
-                                   (6200, 640, 2304)])
+                                   (6200, 640, 2304), (1000, 7168, 2048)])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 def test_gated_ffn_backward(ops, T, d, f, out_dtype):
     say("gated_ffn_backward", T, d, f, out_dtype)
@@ -649,7 +650,8 @@ def test_graph_replay_of_a_block(ops, T):
 def test_two_streams_at_once(ops, T):
     d, f = 640, 1024
     a, b = _ffn_inputs(T, d, f, 1), _ffn_inputs(T, d, f, 2)
-    want = [ops.gated_ffn(*v[:3], v[3]) for v in (a, b)]
+    want = [ops.gated_ffn(*v[:3], v[3], keep=True) for v in (a, b)]
+    grads = [ops.gated_ffn_backward(v[3], v[0], w[1], *v[1:3]) for v, w in zip((a, b), want)]
     torch.cuda.synchronize()
     say("two streams", T)
     s = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -657,11 +659,14 @@ def test_two_streams_at_once(ops, T):
     for _ in range(5):
         for i, v in enumerate((a, b)):
             with torch.cuda.stream(s[i]):
-                got[i].append(ops.gated_ffn(*v[:3], v[3]))
+                y, saved = ops.gated_ffn(*v[:3], v[3], keep=True)
+                got[i].append((y, ops.gated_ffn_backward(v[3], v[0], saved, *v[1:3])))
     torch.cuda.synchronize()
     for i in range(2):
-        for y in got[i]:
-            _bits_equal(y, want[i], "beside another stream's calls")
+        for y, g in got[i]:
+            _bits_equal(y, want[i][0], "beside another stream's calls")
+            for k in ("dx", "dw1p", "dw2"):
+                _bits_equal(g[k], grads[i][k], k)
 
 
 def test_the_block_around_the_layer(ops):
