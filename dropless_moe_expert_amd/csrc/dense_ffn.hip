@@ -308,11 +308,14 @@ __device__ __forceinline__ void tile(const Prod& a, int block, uint8_t* lds) {
   static_assert(!QKO || BM == 128, "K-outer rows are 128 columns");
   constexpr int TM = BM / 32, TN = BN / 32, RING = ring<BM>(), STAGE = stage_bytes<BM>(), QOFF = BN * 128;
   constexpr int NOUT = MODE == GATE ? BN / 2 : BN;   // output columns of the tile
-  // consecutive workgroups run on different XCDs; the m-tiles of one P tile
-  // follow each other on one XCD, so its L2 reads the weights once
-  const int xcd = block & 7, seq = block >> 3;
-  const int mt = seq % a.mtiles, unit = (seq / a.mtiles) * 8 + xcd;
-  if (unit >= a.ntiles * a.S) return;
+  // Consecutive workgroups run on different XCDs: each XCD takes an eighth of
+  // the tiles, the m-tiles of one P tile after each other, so that its L2 reads
+  // the weights once.
+  const int64_t tiles = (int64_t)a.mtiles * a.ntiles * a.S;
+  const int xcd = block & 7;
+  const int64_t id = tiles * xcd / 8 + (block >> 3);
+  if (id >= tiles * (xcd + 1) / 8) return;
+  const int unit = (int)(id / a.mtiles), mt = (int)(id - (int64_t)unit * a.mtiles);
   const int nt = unit % a.ntiles, split = unit / a.ntiles;
   const int m0 = mt * BM, n0 = nt * NOUT;
   const int stages = (a.K + 63) / 64;
@@ -633,7 +636,7 @@ int64_t lay_out(Mode mode, Prod& a, const Plan& p) {
   if (p.S == 1) a.part = nullptr;
   a.mtiles = (a.M + p.BM - 1) / p.BM;
   a.ntiles = (a.N + nout - 1) / nout;
-  return 8 * (int64_t)a.mtiles * (((int64_t)a.ntiles * a.S + 7) / 8);
+  return 8 * (((int64_t)a.mtiles * a.ntiles * a.S + 7) / 8);
 }
 
 template <int MODE>
@@ -825,7 +828,7 @@ extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const 
   // dgu = swiglu'(gu, dy W2)
   if (T > 0) {
     if (p.dgu.form == MANY) {
-      st = launch_fwd(one_group(dy, w2, dgu, const_cast<uint16_t*>(gu), T, f, d, rows, part), MOE_EPI_SWIGLU_BWD, 0,
+      st = launch_fwd(one_group(dy, w2, dgu, const_cast<uint16_t*>(gu), T, f, d, rows, nullptr), kEpiSwigluBwdWide, 0,
                       MOE_B_KN, s);
     } else {
       Prod a = product(w2, f, dy, d, dgu, T, f, d, part);

@@ -343,6 +343,73 @@ __device__ __forceinline__ void store_staged(const GGArgs& a, f32x4_t (&acc)[TN]
   }
 }
 
+// SwiGLU's backward of the tile's dh in fp32 (store_staged's ST_BWD rounds dh to
+// bf16 on its way through LDS, and dgu again: two roundings, and gradients 1.7
+// times as far off as one): the 256 rows of fp32 do not fit LDS, so the row slots
+// go through it two at a time, 128 rows of 1 KB in the four stage buffers,
+// 16-byte units XOR-swizzled by row.
+template <int ACT>
+__device__ __forceinline__ void store_dgu_wide(const GGArgs& a, f32x4_t (&acc)[TN][TM], int64_t m0, int rows, int n0,
+                                               int f, int xrow0, uint8_t* s0, uint8_t* s1, uint8_t* s2, uint8_t* s3) {
+  auto buf = [&](int i) { return i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : s3; };
+  const int lane = threadIdx.x & 63;
+  int wn, wm;
+  wave_pos(wn, wm);
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const int64_t ld2 = 2 * (int64_t)f;
+  const uint8_t* const gbase = a.Caux + m0 * ld2 * 2;
+  uint8_t* const cbase = a.C + m0 * ld2 * 2;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const int slot = xrow0 / WTM - 2 * pass;   // of this pass: 0 or 1
+    if (slot == 0 || slot == 1) {
+#pragma unroll
+      for (int j = 0; j < ACT; ++j) {
+        const int rl = j * 16 + r16;
+        uint8_t* const row = buf(2 * slot + (rl >> 5)) + (rl & 31) * 1024;
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+          *reinterpret_cast<f32x4_t*>(row + (((wn * (WTN / 4) + i * 4 + g4) ^ r16) << 4)) = acc[i][j];
+      }
+    }
+    __syncthreads();
+    constexpr int NPT = (BM / 2) * (BN / 8) / THREADS, NB = 2;   // 8-column pieces per thread
+    static_assert((BM / 2) * (BN / 8) % THREADS == 0 && NPT % NB == 0, "whole batches");
+#pragma unroll 1
+    for (int k0 = 0; k0 < NPT; k0 += NB) {
+      uint4 gv[NB], uv[NB];
+      uint32_t o[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int c = threadIdx.x + (k0 + k) * THREADS;
+        const int row = pass * (BM / 2) + c / (BN / 8), col = n0 + 8 * (c % (BN / 8));
+        o[k] = row < rows && col < f ? (uint32_t)(row * ld2 + col) * 2u : 0xFFFFFFFFu;
+        if (o[k] != 0xFFFFFFFFu) {
+          gv[k] = *reinterpret_cast<const uint4*>(gbase + o[k]);
+          uv[k] = *reinterpret_cast<const uint4*>(gbase + o[k] + (uint32_t)f * 2u);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (o[k] == 0xFFFFFFFFu) continue;
+        const int c = threadIdx.x + (k0 + k) * THREADS;
+        const int rl = c / (BN / 8), u = 2 * (c % (BN / 8));
+        const uint8_t* const row = buf(rl >> 5) + (rl & 31) * 1024;
+        const f32x4_t d0 = *reinterpret_cast<const f32x4_t*>(row + ((u ^ (rl & 15)) << 4));
+        const f32x4_t d1 = *reinterpret_cast<const f32x4_t*>(row + (((u + 1) ^ (rl & 15)) << 4));
+        float g[8], uu[8], dg[8], du[8];
+        unpack8(gv[k], g);
+        unpack8(uv[k], uu);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) swiglu_grad(g[e], uu[e], e < 4 ? d0[e & 3] : d1[e & 3], dg[e], du[e]);
+        *reinterpret_cast<uint4*>(cbase + o[k]) = pack8(dg);
+        *reinterpret_cast<uint4*>(cbase + o[k] + (uint32_t)f * 2u) = pack8(du);
+      }
+    }
+    if (pass == 0) __syncthreads();
+  }
+}
+
 // ------------------------------------------------------------------ split tail
 // (split_tail and its counters: gg_pipeline.h)
 __device__ SplitSlots g_split_sched = initial_split_slots();
@@ -594,6 +661,8 @@ __global__ void __launch_bounds__(THREADS, 1) gg_fwd_kernel(GGArgs a) {
         store_staged<ST_AUX, ACT>(a, acc, m0, rows, n0, 0, f, xrow0, b0, b1, b2, b3);
         __syncthreads();
         store_staged<ST_H, ACT>(a, acc, m0, rows, n0, 0, f, xrow0, b0, b1, b2, b3, hp);
+      } else if constexpr (OUT == MOE_OUT_BF16 && EPI == kEpiSwigluBwdWide) {
+        store_dgu_wide<ACT>(a, acc, m0, rows, n0, a.N, xrow0, b0, b1, b2, b3);
       } else if constexpr (OUT == MOE_OUT_BF16 && EPI == MOE_EPI_SWIGLU_BWD) {
         store_staged<ST_BWD, ACT>(a, acc, m0, rows, n0, a.N, f, xrow0, b0, b1, b2, b3);
       } else if constexpr (OUT == MOE_OUT_BF16) {
@@ -903,6 +972,8 @@ moe_status_t launch_fwd(const GGArgs& a, int epilogue, int out_f32, int b_layout
     if (epilogue == MOE_EPI_SWIGLU) return MOE_ERR_UNSUPPORTED;
     if (epilogue == MOE_EPI_SWIGLU_BWD) {
       hipLaunchKernelGGL((gg_fwd_kernel<MOE_EPI_SWIGLU_BWD, MOE_OUT_BF16, BL_KN>), g, t, 0, s, b);
+    } else if (epilogue == kEpiSwigluBwdWide) {
+      hipLaunchKernelGGL((gg_fwd_kernel<kEpiSwigluBwdWide, MOE_OUT_BF16, BL_KN>), g, t, 0, s, b);
     } else if (out_f32) {
       hipLaunchKernelGGL((gg_fwd_kernel<MOE_EPI_NONE, MOE_OUT_F32, BL_KN>), g, t, 0, s, b);
     } else {

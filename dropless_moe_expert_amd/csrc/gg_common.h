@@ -8,6 +8,9 @@ namespace moe {
 
 constexpr int kMaxGroups = 1024;
 enum { MODE_M_NK = 0, MODE_M_KN = 1, MODE_K = 2 };
+// launch_fwd's epilogue beside the public ones: MOE_EPI_SWIGLU_BWD from the
+// unrounded dh (B_KN, bf16 output, no split tail: part NULL)
+constexpr int kEpiSwigluBwdWide = 9;
 
 struct GGArgs {
   const uint8_t* A;        // activations (bytes)

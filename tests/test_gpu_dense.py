@@ -279,7 +279,7 @@ def _check_ffn_bwd(ops, dy, x, saved, w1, w2, out_dtype):
     f = w2.shape[1]
     DY, X, GU, H, W1, W2 = (f64(t) for t in (dy, x, saved["gu"], saved["h"], w1, w2))
     dh = DY @ W2
-    e = d * ULP32 * (np.abs(DY) @ np.abs(W2)) + ULP16 * np.abs(dh)      # dh, rounded to bf16 at most once
+    e = d * ULP32 * (np.abs(DY) @ np.abs(W2))      # dh is not rounded
     dgu = R.dswiglu(GU, dh)
     lin = np.abs(R.dswiglu(GU, np.ones_like(dh)))
     mag = np.concatenate([np.abs(GU[:, f:]) * (1 + np.abs(GU[:, :f])), np.abs(GU[:, :f])], 1) * np.tile(np.abs(dh), 2)
