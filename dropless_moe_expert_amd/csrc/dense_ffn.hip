@@ -514,22 +514,23 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Prod a) {
 }
 
 // What follows dgu in the backward, in one launch: dx and both weight
-// gradients are independent, and together they fill the chip.
+// gradients are independent, and together they fill the chip.  Workgroups start
+// in order, so the products with the longer tiles come first.
 struct Backward {
   Prod dx, dw1, dw2;
-  int blocks_dx, blocks_dw1;
+  int at_dx, at_dw1, at_dw2;   // first workgroup of each product
+  int n_dx, n_dw1;             // workgroups of the first two
 };
 template <int BM>
 __global__ __launch_bounds__(kTileThreads, 2) void backward_kernel(Backward a) {
   __shared__ __align__(1024) uint8_t lds[std::max(tile_lds<BM>(), tile_lds<128>())];
-  int b = (int)blockIdx.x;
-  if (b < a.blocks_dx) {
-    tile<BM, DX>(a.dx, b, lds);
+  const int b = (int)blockIdx.x;
+  if (b >= a.at_dx && b < a.at_dx + a.n_dx) {
+    tile<BM, DX>(a.dx, b - a.at_dx, lds);
     return;
   }
-  b -= a.blocks_dx;
-  const bool first = b < a.blocks_dw1;
-  tile<128, WGRAD>(first ? a.dw1 : a.dw2, first ? b : b - a.blocks_dw1, lds);
+  const bool first = b >= a.at_dw1 && b < a.at_dw1 + a.n_dw1;
+  tile<128, WGRAD>(first ? a.dw1 : a.dw2, b - (first ? a.at_dw1 : a.at_dw2), lds);
 }
 
 // The partial sums of the S splits, added in split order, through the
@@ -871,8 +872,12 @@ extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const 
   const int64_t all = blocks[0] + blocks[1] + blocks[2];
   if (all == 0) return MOE_OK;
   if (all > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  b.blocks_dx = (int)blocks[0];
-  b.blocks_dw1 = (int)blocks[1];
+  const bool dx_first = (2 * (int64_t)f + b.dx.S - 1) / std::max(b.dx.S, 1) >= T;
+  b.n_dx = (int)blocks[0];
+  b.n_dw1 = (int)blocks[1];
+  b.at_dx = dx_first ? 0 : (int)(blocks[1] + blocks[2]);
+  b.at_dw1 = dx_first ? (int)blocks[0] : 0;
+  b.at_dw2 = b.at_dw1 + (int)blocks[1];
   if (p.rest[0].form == TILES && p.rest[0].BM == 64) {
     hipLaunchKernelGGL((backward_kernel<64>), dim3((unsigned)all), dim3(kTileThreads), 0, s, b);
   } else {

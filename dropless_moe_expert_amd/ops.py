@@ -921,6 +921,7 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step: torch.Tensor, *, lr: fl
     step, tensor, element).  step: int32 [1] on the GPU, advanced by one.
     grad_scale: fp32 [1] on the GPU; infinite or NaN: the step is skipped."""
     n = len(params)
+    _need(len(grads) == n and not any([t is None for t in params]), "params, grads: lists of as many tensors")
     _need(step.is_cuda and step.dtype == torch.int32 and step.numel() == 1, "step: int32 [1] on the GPU")
     dev = step.device
     index = dev.index
@@ -947,7 +948,7 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step: torch.Tensor, *, lr: fl
         if ts is None:
             table[k::8] = [0] * n
             continue
-        if len(ts) != n:
+        if len(ts) != n or any([t is None for t in ts]):
             raise MoeError(what + ": one tensor for each of params")
         want = numels if k < 5 else [(m + 31) // 32 for m in numels]
         if [t.numel() for t in ts] != want or not all([t.dtype in types and t.get_device() == index and t.is_contiguous()

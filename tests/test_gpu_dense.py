@@ -572,7 +572,8 @@ def test_adamw_refuses(ops):
     for k, v in (("params", [st["params"][0]] * 2), ("exp_avg", st["exp_avg"][:1]), ("step", st["step"].cpu()),
                  ("grads", [st["grads"][0], st["grads"][1].float()]), ("exp_avg", [t.half() for t in st["exp_avg"]]),
                  ("masters", [t[:32] for t in st["masters"]]), ("exp_avg_scale", st["exp_avg"]),
-                 ("params", [t.view(8, 8).t() for t in st["params"]])):
+                 ("params", [t.view(8, 8).t() for t in st["params"]]), ("grads", [st["grads"][0], None]),
+                 ("grads", st["grads"][:1]), ("exp_avg_sq", [None, None])):
         bad = dict(st)
         bad[k] = v
         with pytest.raises(ops.MoeError):
