@@ -59,7 +59,7 @@ enum { BL_NK = 0, BL_PACKED = 1, BL_KN = 2 };
 // (C_aux != NULL); its own instantiation keeps the h-only SwiGLU kernel lean
 constexpr int EPI_SWIGLU_AUX = 7;
 // kernel-internal epilogue: C = bf16(residual + A Bop), the residual bf16
-// rows in C_aux (pitch ld_aux) loaded into the accumulators, so that the sum
+// rows in C_aux (pitch M) loaded into the accumulators, so that the sum
 // is rounded once
 constexpr int EPI_RESIDUAL = 8;
 static_assert(EPI_SWIGLU_AUX != MOE_EPI_NONE && EPI_SWIGLU_AUX != MOE_EPI_SWIGLU &&
@@ -343,11 +343,12 @@ __device__ __forceinline__ void store_staged(const GGArgs& a, f32x4_t (&acc)[TN]
   }
 }
 
-// SwiGLU's backward of the tile's dh in fp32 (store_staged's ST_BWD rounds dh to
-// bf16 on its way through LDS, and dgu again: two roundings, and gradients 1.7
-// times as far off as one): the 256 rows of fp32 do not fit LDS, so the row slots
-// go through it two at a time, 128 rows of 1 KB in the four stage buffers,
-// 16-byte units XOR-swizzled by row.
+// SwiGLU's backward of the tile's dh in fp32, for the dense block: store_staged's
+// ST_BWD rounds dh to bf16 on its way through LDS and then dgu, which leaves dx
+// 2.9e-3 from the exact one (relative, 2-norm); rounding dgu alone 2.3e-3, and
+// the launch takes 2 % longer (8192 tokens, d = 7168, f = 2048).  256 rows of
+// fp32 do not fit LDS, so the row slots go through it two at a time, 128 rows of
+// 1 KB in the four stage buffers, 16-byte units XOR-swizzled by row.
 template <int ACT>
 __device__ __forceinline__ void store_dgu_wide(const GGArgs& a, f32x4_t (&acc)[TN][TM], int64_t m0, int rows, int n0,
                                                int f, int xrow0, uint8_t* s0, uint8_t* s1, uint8_t* s2, uint8_t* s3) {
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(THREADS, 1) gg_fwd_kernel(GGArgs a) {
         // in flight together with the first stages
         {
           const int lane = threadIdx.x & 63;
-          const uint16_t* const res = reinterpret_cast<const uint16_t*>(a.Caux) + m0 * a.ld_aux;
+          const uint16_t* const res = reinterpret_cast<const uint16_t*>(a.Caux) + m0 * a.M;
 #pragma unroll
           for (int j = 0; j < ACT; ++j) {
             const int mr = xrow0 + j * 16 + (lane & 15);
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1) gg_fwd_kernel(GGArgs a) {
             for (int i = 0; i < TN; ++i) {
               const int n = n0 + wn_ * WTN + i * 16 + 4 * (lane >> 4);
               if (mr < rows && n < a.N) {
-                const uint2 v = *reinterpret_cast<const uint2*>(res + mr * a.ld_aux + n);
+                const uint2 v = *reinterpret_cast<const uint2*>(res + (int64_t)mr * a.M + n);
                 acc[i][j] = f32x4_t{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
                                     __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u)};
               }
@@ -1002,7 +1003,7 @@ moe_status_t launch_fwd(const GGArgs& a, int epilogue, int out_f32, int b_layout
 }
 
 // bf16, one dense product with the residual in its accumulators (B [1, N, K],
-// C_aux = the residual, pitch ld_aux)
+// C_aux = the residual, pitch M)
 moe_status_t launch_fwd_residual(const GGArgs& a, hipStream_t s) {
   using namespace fwd;
   GGArgs b = a;

@@ -22,14 +22,13 @@ struct GGArgs {
   uint8_t* Caux;
   uint32_t* flag;
   int64_t m_cap;
-  int G, M, N, K;
+  int G, M, N, K;          // M: ragged-K rows of C[g]; launch_fwd_residual: row pitch of the residual in Caux
   int n_tiles;             // tiles along n (ragged-M) / q (ragged-K)
   int p_tiles;             // ragged-K: tiles along p (rows of C[g])
   int sched_slot;          // the launch's slot of tile-queue (ragged-K) or split (ragged-M) words
   uint32_t sched_epoch;    // the launch's epoch (tile_queue.h)
   uint32_t sched_next;     // the epoch of the slot's next launch
   float* part;             // ragged-M bf16: workspace of the split tail's partial sums, or NULL
-  int64_t ld_aux;          // row pitch of the residual in Caux (launch_fwd_residual only)
 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
