@@ -61,11 +61,15 @@ __device__ __forceinline__ f32x4_t mfma(uint4 w, uint4 x, f32x4_t c) {
 
 // ------------------------------------------------------------------ few tokens
 // 16 weight rows per workgroup (gated: 8 gate rows and the 8 matching up
-// rows), MT x 16 tokens.  Wavefront w takes the 32-deep K steps w, w + NW, ...,
-// U of them in flight while the U before are multiplied.
-constexpr int kFewWaves = 8, kFewUnroll = 8;
+// rows), up to 16 tokens.  Wavefront w takes the 32-deep K steps w, w + NW, ...,
+// U of them in flight while the U before are multiplied: 40 to 80 KB a compute
+// unit, and registers for two workgroups on one.  One token, d = 7168, f = 2048
+// (88 MB of weights): 18.9 us, 4.7 TB/s; U = 8 19.9, 4 19.1, 16 wavefronts 19.7,
+// 4 wavefronts 20.0, non-temporal loads 22.7.  d = 4096, f = 14336: 67.6 us, 5.2
+// TB/s, above a plain copy's 5.0.
+constexpr int kFewWaves = 8, kFewUnroll = 5;
 
-template <int MT, bool GATED>
+template <bool GATED>
 __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(Prod a) {
   constexpr int NW = kFewWaves, U = kFewUnroll;
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -78,15 +82,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(Prod a) {
     row = min(n0 + r16, a.N - 1);
   }
   const uint16_t* wp = a.p + (int64_t)row * a.ldp + 8 * g4;
-  const uint16_t* xp[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) xp[m] = a.q + (int64_t)min(16 * m + r16, a.M - 1) * a.ldq + 8 * g4;
+  const uint16_t* xp = a.q + (int64_t)min(r16, a.M - 1) * a.ldq + 8 * g4;
   const int steps = (a.K + 31) / 32;
-  f32x4_t acc[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
   struct Batch {
-    uint4 w[U], x[U][MT];
+    uint4 w[U], x[U];
   };
   auto load = [&](int s0, Batch& b) {
 #pragma unroll
@@ -94,16 +94,12 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(Prod a) {
       const int k = 32 * (s0 + u * NW);
       const bool ok = k + 8 * g4 < a.K;   // K % 8 == 0: a lane's piece is whole or absent
       b.w[u] = ok ? *reinterpret_cast<const uint4*>(wp + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-        b.x[u][m] = ok ? *reinterpret_cast<const uint4*>(xp[m] + k) : make_uint4(0, 0, 0, 0);
+      b.x[u] = ok ? *reinterpret_cast<const uint4*>(xp + k) : make_uint4(0, 0, 0, 0);
     }
   };
   auto mma = [&](const Batch& b) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[m] = mfma(b.w[u], b.x[u][m], acc[m]);
+    for (int u = 0; u < U; ++u) acc = mfma(b.w[u], b.x[u], acc);
   };
   Batch p, q;
   int s = wave;
@@ -118,14 +114,12 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(Prod a) {
     mma(q);
   }
   // sum of the wavefronts in their order; lane: token r16, rows 4 g4 + e
-  __shared__ float sum[NW][MT * 16][17];
+  __shared__ float sum[NW][16][17];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[wave][16 * m + r16][4 * g4 + e] = acc[m][e];
+  for (int e = 0; e < 4; ++e) sum[wave][r16][4 * g4 + e] = acc[e];
   __syncthreads();
   constexpr int PER = GATED ? 8 : 16;   // output columns of the workgroup
-  for (int i = threadIdx.x; i < MT * 16 * PER; i += NW * 64) {
+  for (int i = threadIdx.x; i < 16 * PER; i += NW * 64) {
     const int t = i / PER, j = i % PER;
     if (t >= a.M || n0 + j >= a.N) continue;
     float v = 0.f, u = 0.f;
@@ -770,7 +764,7 @@ extern "C" moe_status_t moe_gated_ffn_launch(const uint16_t* x, int64_t ldx, con
   a.aux = gu;
   moe_status_t st;
   if (p1.form == FEW) {
-    hipLaunchKernelGGL((few_tokens_kernel<1, true>), dim3((unsigned)((f + 7) / 8)), dim3(kFewWaves * 64), 0, s, a);
+    hipLaunchKernelGGL((few_tokens_kernel<true>), dim3((unsigned)((f + 7) / 8)), dim3(kFewWaves * 64), 0, s, a);
     st = ffn::status();
   } else if (p1.form == TILES) {
     st = run_tiles<GATE>(a, p1, s);
@@ -782,7 +776,7 @@ extern "C" moe_status_t moe_gated_ffn_launch(const uint16_t* x, int64_t ldx, con
   b.res = res;
   b.ldr = ldr;
   if (p2.form == FEW) {
-    hipLaunchKernelGGL((few_tokens_kernel<1, false>), dim3((unsigned)((d + 15) / 16)), dim3(kFewWaves * 64), 0, s, b);
+    hipLaunchKernelGGL((few_tokens_kernel<false>), dim3((unsigned)((d + 15) / 16)), dim3(kFewWaves * 64), 0, s, b);
     return ffn::status();
   }
   if (p2.form == TILES) return run_tiles<DOWN>(b, p2, s);

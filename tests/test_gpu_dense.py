@@ -582,6 +582,100 @@ def test_adamw_refuses(ops):
         _call(ops, st, betas=(1.0, 0.9))
 
 
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def test_norm_past_32_bit_offsets(ops):
+    """More than 2^31 elements (and, in fp32, 2^33 bytes): the last rows are the small call's."""
+    T, d = 330_000, 6560
+    x = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    r = torch.zeros((T, d), dtype=torch.float32, device="cuda")
+    rng = np.random.default_rng(21)
+    tail = 40
+    x[-tail:], r[-tail:] = _t(rng, (tail, d)), _t(rng, (tail, d), torch.float32)
+    w = _t(rng, (d,))
+    say("norm past 32 bits")
+    big = ops.add_rmsnorm(x, w, r, mxfp8=True, keep_rstd=True)
+    small = ops.add_rmsnorm(x[-tail:].clone(), w, r[-tail:].clone(), mxfp8=True, keep_rstd=True)
+    # a wavefront's and a workgroup's sums of one row differ in order: the same bound as against 64 bits
+    _within(big["rstd"][-tail:], f64(small["rstd"]), 62 * ULP32 * f64(small["rstd"]), "rstd")
+    for k in ("y", "s"):
+        _within(big[k][-tail:], f64(small[k]), 2 * ULP16 * np.abs(f64(small[k])), k)
+        assert not big[k][:-tail].any(), k
+    q, sc = ops.mxfp8_quantize(big["y"][-tail:].clone(), 0)
+    _bits_equal(big["q"][-tail:], q, "codes")
+    _bits_equal(big["scale"][-tail:], sc, "scales")
+    dy = torch.zeros_like(x)
+    dy[-tail:] = _t(rng, (tail, d))
+    b = ops.add_rmsnorm_backward(dy, big["s"], w, big["rstd"], dresidual=r)
+    D, S, K = f64(dy[-tail:]), f64(big["s"][-tail:]), f64(big["rstd"][-tail:])
+    ds, dw = R.rmsnorm_backward(D, S, f64(w), K, f64(r[-tail:]))
+    _within(b["ds"][-tail:], ds, 80 * ULP32 * (np.abs(ds) + K[:, None] * np.abs(f64(w) * D) + np.abs(S * K[:, None])), "ds")
+    _within(b["dweight"], dw, (T // 512 + 131) * ULP32 * np.abs(D * S * K[:, None]).sum(0), "dweight")
+
+
+@pytest.mark.parametrize("pitch", [0, 8])
+def test_ffn_past_32_bit_offsets(ops, pitch):
+    T, d, f = 1_100_000, 64, 1024        # gu: 2.25e9 elements
+    rng = np.random.default_rng(22)
+    w1, w2 = _t(rng, (2 * f, d), scale=d ** -0.5), _t(rng, (d, f), scale=f ** -0.5)
+    x = torch.zeros((T, d + pitch), dtype=torch.bfloat16, device="cuda")[:, :d]
+    tail = 70
+    x[-tail:] = _t(rng, (tail, d))
+    say("ffn past 32 bits", pitch)
+    y, saved = ops.gated_ffn(x, w1, w2, x, keep=True)
+    _, h, gu = R.ffn(f64(x[-tail:]), f64(w1), f64(w2))
+    e = d * ULP32 * (np.abs(f64(x[-tail:])) @ np.abs(f64(w1)).T)
+    _within(saved["gu"][-tail:], gu, ULP16 * np.abs(gu) + e * (1 + ULP16), "gu")
+    H = f64(saved["h"][-tail:])
+    yr = H @ f64(w2).T + f64(x[-tail:])
+    _within(y[-tail:], yr, ULP16 * np.abs(yr) + 1.01 * (f + 2) * ULP32 * (np.abs(H) @ np.abs(f64(w2)).T + np.abs(f64(x[-tail:]))),
+            "y")
+    assert not y[:-tail].any() and not saved["h"][:-tail].any()
+    if pitch:
+        return
+    dy = torch.zeros_like(y)
+    dy[-tail:] = _t(rng, (tail, d))
+    o = ops.gated_ffn_backward(dy, x, saved, w1, w2)
+    cut = {k: saved[k][-tail:].clone() for k in saved}
+    p = ops.gated_ffn_backward(dy[-tail:].clone(), x[-tail:].clone(), cut, w1, w2)
+    G = f64(p["dgu"])
+    _within(o["dgu"][-tail:], G, 2 * ULP16 * np.abs(G) + 2.0 ** -126, "dgu")
+    dw1 = f64(o["dgu"][-tail:]).T @ f64(x[-tail:])
+    _within(o["dw1p"], dw1, ULP16 * np.abs(dw1) + 1.01 * tail * ULP32 * (np.abs(G).T @ np.abs(f64(x[-tail:]))) + 2.0 ** -126, "dw1p")
+
+
+def test_adamw_past_32_bit_elements(ops):
+    """An element's random bits and its block lie where its 64-bit index says."""
+    n, tail = (1 << 32) + 3001, 5000
+    rng = np.random.default_rng(23)
+    dev = torch.device("cuda")
+    p = torch.zeros(n, dtype=torch.bfloat16, device=dev)
+    g = torch.zeros(n, dtype=torch.bfloat16, device=dev)
+    p[-tail:], g[-tail:] = _t(rng, (tail,), scale=0.05), _t(rng, (tail,), scale=1e-2)
+    st = ops.adamw_state([p], 8)
+    before = p[-tail:].clone()
+    say("adamw past 32 bits")
+    ops.adamw_step([p], [g], st["exp_avg"], st["exp_avg_sq"], st["step"], exp_avg_scale=st["exp_avg_scale"],
+                   exp_avg_sq_scale=st["exp_avg_sq_scale"], seed=11, **HYPER)
+    torch.cuda.synchronize()
+    i = np.arange(n - tail, n, dtype=np.uint64)
+    key = R.mix(R.mix(R.mix(11) ^ np.uint64(1)) ^ np.uint64(0))
+    r = R.mix((i & np.uint64(0xFFFFFFFF)) + R.mix(key ^ (i >> np.uint64(32))))
+    want, m, v = R.adamw(f64(before), f64(g[-tail:]), 0.0, 0.0, 1, HYPER["lr"], *HYPER["betas"], HYPER["eps"],
+                         HYPER["weight_decay"])
+    ep = 4 * ULP32 * np.abs(f64(before)) + HYPER["lr"] * 40 * ULP32
+    r16 = R.mix(r + np.uint64(0x9E3779B9)) & np.uint64(0xFFFF)
+    a, b = R.bf16_random((want - ep).astype(np.float32), r16), R.bf16_random((want + ep).astype(np.float32), r16)
+    got = f64(p[-tail:])
+    assert ((np.minimum(a, b) <= got) & (got <= np.maximum(a, b))).all()
+    assert not p[:-tail].any() and not st["exp_avg"][0].view(torch.uint8)[:-tail].any()
+    # whole blocks of the tail: their codes from the same bits
+    skip = -(n - tail) % 32
+    at = (n - tail + skip) // 32
+    _check_codes(st["exp_avg"][0][n - tail + skip:], st["exp_avg_scale"][0][at:], m[skip:], 8 * ULP32 * np.abs(m[skip:]),
+                 r[skip:] & np.uint64(0xFFFF), "m codes")
+
+
 # ------------------------------------------------------------------ as they are used
 
 def _replayed(make, run, outputs, other):
