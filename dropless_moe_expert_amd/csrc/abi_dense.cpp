@@ -61,6 +61,8 @@ moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ldx, const void* w, int3
   if (T == 0) return MOE_OK;
   if (!x || !w || (!y && !q)) return MOE_ERR_INVALID_ARG;
   if (ldx < d || (r && (ldr < d || lds < d))) return MOE_ERR_INVALID_ARG;
+  // in place: the rows must be the same ones
+  if (T > 1 && r && ((s == r && lds != ldr) || (s == x && lds != ldx))) return MOE_ERR_INVALID_ARG;
   const unsigned rb = width(r_dtype);
   if (!aligned(x, 2) || !aligned(w, width(w_dtype)) || !aligned(y, 2) || !aligned(rstd, 4) ||
       (r && (!aligned(r, rb) || !aligned(s, rb))))
@@ -103,6 +105,7 @@ moe_status_t moe_add_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const vo
   if ((s_dtype == MOE_OUT_F32) != (ds != nullptr) && T > 0) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!dy || !s || !w || !rstd || !dx)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (lddy < d || lds < d || (dres && lddres < d))) return MOE_ERR_INVALID_ARG;
+  if (T > 1 && dx == dy && lddy != d) return MOE_ERR_INVALID_ARG;
   const unsigned sb = width(s_dtype);
   if (!aligned(dw, 4)) return MOE_ERR_ALIGNMENT;
   if (T > 0 && (!aligned(dy, 2) || !aligned(s, sb) || !aligned(w, width(w_dtype)) || !aligned(rstd, 4) ||
@@ -144,7 +147,7 @@ moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, 
   if (!x || !w1p || !w2 || !y || (gu && !h) || y == x) return MOE_ERR_INVALID_ARG;
   if (ldx < d || (res && ldres < d) || (res == y && res && ldres != d)) return MOE_ERR_INVALID_ARG;
   if (ldx % 8 || (res && ldres % 8)) return MOE_ERR_ALIGNMENT;
-  // 128 rows' byte offsets stay in 32 bits
+  // 256 rows' byte offsets stay in 32 bits
   if (ldx > (1 << 23) || (res && ldres > (1 << 23))) return MOE_ERR_UNSUPPORTED;
   if (!aligned(x, 16) || !aligned(w1p, 16) || !aligned(w2, 16) || !aligned(res, 16) || !aligned(h, 16) ||
       !aligned(gu, 16) || !aligned(y, 16))

@@ -6,7 +6,10 @@
 // Bound: HBM (28 bytes an element with fp32 states, master weights and bf16
 // gradients; 10.1 with 8-bit states and bf16 weights).  A workgroup takes one
 // chunk of one tensor; the tensors' addresses travel in the kernel's
-// arguments.  All arithmetic is fp32.
+// arguments.  All arithmetic is fp32.  Measured for 117 M weights in four
+// tensors: fp32 states 621 us, 5.3 TB/s (a plain device copy: 5.0), with
+// non-temporal accesses 659; 8-bit states 236 us, 5.0 TB/s (302 us while the
+// codes were formed by integer arithmetic, 3.9 TB/s: the vector unit's bound).
 //
 // 8-bit states: m and sqrt(v) as E4M3 codes with one E8M0 scale per 32
 // consecutive elements, 2^e the smallest power of two with amax <= 448 * 2^e.

@@ -6,6 +6,13 @@
 
 namespace moe {
 
+// A launch dimension holds fewer than 2^32 threads: workgroup numbers past
+// kGridX continue in y (workgroup = y * kGridX + x), a multiple of 8 that keeps
+// a workgroup's XCD its number modulo 8.
+constexpr int64_t kGridX = 1 << 20;
+inline int64_t grid_x(int64_t workgroups) { return workgroups < kGridX ? workgroups : kGridX; }
+inline int64_t grid_y(int64_t workgroups) { return (workgroups + kGridX - 1) / kGridX; }
+
 enum { RES_NONE = 0, RES_BF16 = 1, RES_F32 = 2 };
 
 struct NormArgs {

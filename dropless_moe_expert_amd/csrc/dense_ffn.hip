@@ -163,6 +163,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_tokens_kernel(Prod a) {
 // Pieces past K are loaded from a page of zeros, rows past M or N repeat the
 // last one and are not stored.
 constexpr int BN = 128;
+// 64-deep stages of a contraction (a weight gradient's may be 2^31 - 1)
+__host__ __device__ constexpr int stages_of(int K) { return (int)(((unsigned)K + 63u) / 64u); }
 constexpr int KO_PITCH = 256;   // bytes of a K-outer row (128 columns)
 
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
@@ -323,7 +325,7 @@ __device__ __forceinline__ void tile(const Prod& a, int block, uint8_t* lds) {
   const int mt = (id < tall ? 0 : a.btall * (a.bh + 1)) + blk * h + at0 - unit * h;
   const int nt = unit % a.ntiles, split = unit / a.ntiles;
   const int m0 = mt * BM, n0 = nt * NOUT;
-  const int stages = (a.K + 63) / 64;
+  const int stages = stages_of(a.K);
   const int s0 = (int)((int64_t)split * stages / a.S), n = (int)((int64_t)(split + 1) * stages / a.S) - s0;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int r16 = lane & 15, g4 = lane >> 4;
@@ -512,10 +514,13 @@ __device__ __forceinline__ void tile(const Prod& a, int block, uint8_t* lds) {
   }
 }
 
+__device__ __forceinline__ int workgroup() { return (int)(blockIdx.y * kGridX + blockIdx.x); }
+dim3 tile_grid(int64_t blocks) { return dim3((unsigned)grid_x(blocks), (unsigned)grid_y(blocks)); }
+
 template <int BM, int MODE>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(Prod a) {
   __shared__ __align__(1024) uint8_t lds[tile_lds<BM>()];
-  tile<BM, MODE>(a, (int)blockIdx.x, lds);
+  tile<BM, MODE>(a, workgroup(), lds);
 }
 
 // What follows dgu in the backward, in one launch: dx and both weight
@@ -529,7 +534,7 @@ struct Backward {
 template <int BM>
 __global__ __launch_bounds__(kTileThreads, 2) void backward_kernel(Backward a) {
   __shared__ __align__(1024) uint8_t lds[std::max(tile_lds<BM>(), tile_lds<128>())];
-  const int b = (int)blockIdx.x;
+  const int b = workgroup();
   if (b >= a.at_dx && b < a.at_dx + a.n_dx) {
     tile<BM, DX>(a.dx, b - a.at_dx, lds);
     return;
@@ -640,7 +645,7 @@ int64_t lay_out(Mode mode, Prod& a, const Plan& p) {
   const int nout = mode == GATE ? BN / 2 : BN;
   a.S = p.S;
   if (p.S == 1) a.part = nullptr;
-  a.mtiles = (a.M + p.BM - 1) / p.BM;
+  a.mtiles = (int)(((int64_t)a.M + p.BM - 1) / p.BM);
   a.ntiles = (a.N + nout - 1) / nout;
   // a block's height: as many rows as its share of the P tiles, of the 32 tiles
   // (or fewer) that one XCD works on at a time
@@ -663,13 +668,13 @@ moe_status_t run_join(const Prod& a, hipStream_t s) {
 template <int MODE>
 moe_status_t run_tiles(Prod a, const Plan& p, hipStream_t s) {
   const int64_t blocks = lay_out((Mode)MODE, a, p);
-  if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (blocks > INT32_MAX - kGridX) return MOE_ERR_UNSUPPORTED;
   if (p.BM == 64) {
-    hipLaunchKernelGGL((tile_kernel<64, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<64, MODE>), tile_grid(blocks), dim3(kTileThreads), 0, s, a);
   } else if (p.BM == 256) {
-    hipLaunchKernelGGL((tile_kernel<256, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<256, MODE>), tile_grid(blocks), dim3(kTileThreads), 0, s, a);
   } else {
-    hipLaunchKernelGGL((tile_kernel<128, MODE>), dim3((unsigned)blocks), dim3(kTileThreads), 0, s, a);
+    hipLaunchKernelGGL((tile_kernel<128, MODE>), tile_grid(blocks), dim3(kTileThreads), 0, s, a);
   }
   if (status() != MOE_OK) return MOE_ERR_HIP;
   return p.S > 1 ? run_join<MODE>(a, s) : MOE_OK;
@@ -732,16 +737,16 @@ BackwardPlan plan_backward(int64_t T, int d, int f) {
     // A tile's first loads and stores take 1.7 us; a 256 x 256 weight gradient's
     // 8, and 16 once (d = 7168, f = 2048: dw2, one round, 256 tokens 29 us, 4096
     // tokens 112; the three of 256 tokens 151 there, 97 as tiles of one launch)
-    one[i] = ((sh[i].K + 63) / 64) * stage_us(sh[i].mode, BM) + 1.7;
+    one[i] = stages_of(sh[i].K) * stage_us(sh[i].mode, BM) + 1.7;
     const double us = (double)tiles_of(sh[i].mode, sh[i].M, sh[i].N, BM) * one[i] / cus;
     const int64_t rounds = ((sh[i].M + 255) / 256 * ((sh[i].N + 255) / 256) + cus - 1) / cus;
-    const double large = 16 + (double)rounds * (((sh[i].K + 31) / 32) * 0.80 + 8);
+    const double large = 16 + (double)rounds * (2 * stages_of(sh[i].K) * 0.80 + 8);
     p.rest[i] = many && large < us ? Plan{MANY, 0, 1} : Plan{TILES, BM, 1};
     if (p.rest[i].form == TILES) work += us;
   }
   for (int i = 0; i < 3; ++i) {
     if (p.rest[i].form != TILES) continue;
-    const int most = std::min(16, std::max(1, (sh[i].K + 63) / 64 / 4));
+    const int most = std::min(16, std::max(1, stages_of(sh[i].K) / 4));
     const int S = std::min(most, (int)std::min(16.0, one[i] / std::max(work, 3.0) + 1));
     if (S > 1 && join_us(sh[i].mode, sh[i].M, sh[i].N, S) < one[i] - std::max(work, one[i] / S)) p.rest[i].S = S;
   }
@@ -883,7 +888,7 @@ extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const 
   }
   const int64_t all = blocks[0] + blocks[1] + blocks[2];
   if (all == 0) return MOE_OK;
-  if (all > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (all > INT32_MAX - kGridX) return MOE_ERR_UNSUPPORTED;
   const bool dx_first = (2 * (int64_t)f + b.dx.S - 1) / std::max(b.dx.S, 1) >= T;
   b.n_dx = (int)blocks[0];
   b.n_dw1 = (int)blocks[1];
@@ -891,9 +896,9 @@ extern "C" moe_status_t moe_gated_ffn_backward_launch(const uint16_t* dy, const 
   b.at_dw1 = dx_first ? (int)blocks[0] : 0;
   b.at_dw2 = b.at_dw1 + (int)blocks[1];
   if (p.rest[0].form == TILES && p.rest[0].BM == 64) {
-    hipLaunchKernelGGL((backward_kernel<64>), dim3((unsigned)all), dim3(kTileThreads), 0, s, b);
+    hipLaunchKernelGGL((backward_kernel<64>), tile_grid(all), dim3(kTileThreads), 0, s, b);
   } else {
-    hipLaunchKernelGGL((backward_kernel<128>), dim3((unsigned)all), dim3(kTileThreads), 0, s, b);
+    hipLaunchKernelGGL((backward_kernel<128>), tile_grid(all), dim3(kTileThreads), 0, s, b);
   }
   if (ffn::status() != MOE_OK) return MOE_ERR_HIP;
   if (blocks[0] && b.dx.S > 1) st = run_join<DX>(b.dx, s);

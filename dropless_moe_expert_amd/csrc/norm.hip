@@ -133,7 +133,7 @@ template <int TPR, int VPT, int RT, bool ANY>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(NormArgs a) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
   const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
+  const int64_t row = (blockIdx.y * kGridX + blockIdx.x) * RPW + threadIdx.x / TPR;
   if (row >= a.T) return;   // RPW > 1: all threads of a row, whose sum has no barrier then
   const int nvec = (a.d + 7) / 8;
   const uint16_t* xr = a.x + row * a.ldx;
@@ -234,9 +234,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(Norm
 // ------------------------------------------------------------------ backward
 
 // Each workgroup walks rows blockIdx, blockIdx + grid, ... (RPW at a time)
-// and keeps its share of dw in registers; the next row's loads are in flight
-// while a row is reduced and written.  The workgroups' sums go to part and
-// are added by norm_dw_kernel in a fixed order: no atomics.
+// and keeps its share of dw in registers, so that dw costs no second pass over
+// dy and s; the next row's loads are in flight while a row is reduced and
+// written.  The workgroups' sums go to part and are added by norm_dw_kernel in a
+// fixed order: no atomics.
 template <int TPR, int VPT, int ST, bool ANY>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_backward_kernel(NormBwdArgs a) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
@@ -387,7 +388,8 @@ template <int RT, bool ANY>
 void launch_norm(const NormArgs& a, hipStream_t s) {
   auto go = [&](auto kern, int tpr) {
     const int rpw = tpr < 256 ? 256 / tpr : 1;
-    hipLaunchKernelGGL(kern, dim3((unsigned)((a.T + rpw - 1) / rpw)), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
+    const int64_t n = (a.T + rpw - 1) / rpw;
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid_x(n), (unsigned)grid_y(n)), dim3(tpr < 256 ? 256 : tpr), 0, s, a);
   };
   const int nvec = (a.d + 7) / 8;
   // few rows: many threads each, for the latency; many rows: a wavefront each

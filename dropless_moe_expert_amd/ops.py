@@ -918,7 +918,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step: torch.Tensor, *, lr: fl
     exp_avg, exp_avg_sq: fp32 m and v, or E4M3 codes of m and sqrt(v) with
     E8M0 scales of 32 elements in exp_avg_scale, exp_avg_sq_scale; bf16 params
     without masters and 8-bit states are rounded at random by a hash of (seed,
-    step, tensor, element).  step: int32 [1] on the GPU, advanced by one.
+    step, tensor, element).  No two tensors may overlap.  step: int32 [1] on
+    the GPU, advanced by one.
     grad_scale: fp32 [1] on the GPU; infinite or NaN: the step is skipped."""
     n = len(params)
     _need(len(grads) == n and not any([t is None for t in params]), "params, grads: lists of as many tensors")

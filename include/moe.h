@@ -496,8 +496,8 @@ moe_status_t moe_swiglu_backward_mxfp8(const uint16_t* gu, const uint16_t* dh, i
  * The norm is that of s as it is stored.  Sums and rstd are fp32.
  *   x [T, d] bf16, pitch ldx;  w [d] bf16 or fp32 (w_dtype MOE_OUT_BF16 /
  *   MOE_OUT_F32);  r [T, d] bf16 or fp32 (r_dtype), pitch ldr, or NULL;
- *   s [T, d] in r's type, pitch lds: required with r (may be r itself: the
- *   residual stream updated in place), NULL without;
+ *   s [T, d] in r's type, pitch lds: required with r (may be r itself, with
+ *   lds = ldr: the residual stream updated in place), NULL without;
  *   y [T, d] bf16 or NULL;  q uint8 [T, d] with q_scale uint8 [T, d/32], both
  *   or neither: bit for bit mxfp8_group_quantize (axis 0) of y, written
  *   whether or not y is; y and q may not both be NULL;
@@ -543,7 +543,10 @@ moe_status_t moe_add_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const vo
  * Every T >= 0 runs, a single token included (T <= 16 reads the weights once,
  * straight into the matrix instructions' operands).  Results do not depend on
  * thread timing.  Limits: d % 8 == 0, f % 8 == 0, 8 <= d, f <= 2^20,
- * 2 f d < 2^31, T < 2^31, pitches <= 2^23; all pointers 16-byte aligned. */
+ * 2 f d < 2^31, T < 2^31, pitches <= 2^23; all pointers 16-byte aligned.
+ * With many tokens (d % 64 == 0, f % 64 == 0) each product takes one of the 64
+ * slots of arrival counters of RAGGED_M grouped_gemm; what is said of RAGGED_K
+ * about calls in flight and about one graph on two streams holds for them. */
 size_t moe_gated_ffn_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t keep_h, int32_t strided_x);
 moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, const uint16_t* w2,
                            const uint16_t* res, int64_t ldres, int64_t T, int32_t d, int32_t f, uint16_t* h,
@@ -557,9 +560,10 @@ moe_status_t moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* w1p, 
  * aligned.  ws: moe_gated_ffn_backward_workspace_bytes(T, d, f), 256-byte
  * aligned; calls in flight together must not share it.  T = 0 gives zero
  * weight gradients.  Sizes as the forward (d % 64 == 0 and f % 32 == 0 let many
- * tokens run on the kernels of the grouped products; their weight gradients
- * take two of the 64 queue slots of RAGGED_K grouped_gemm: what is said there
- * about calls in flight and about one graph on two streams holds here). */
+ * tokens run on the kernels of the grouped products; dx takes one of the 64
+ * slots of RAGGED_M grouped_gemm and the weight gradients two of RAGGED_K's:
+ * what is said there about calls in flight and about one graph on two streams
+ * holds here). */
 size_t moe_gated_ffn_backward_workspace_bytes(int64_t T, int32_t d, int32_t f);
 moe_status_t moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* gu, const uint16_t* h,
                                     const uint16_t* w1p, const uint16_t* w2, int64_t T, int32_t d, int32_t f,
@@ -571,9 +575,9 @@ moe_status_t moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, const
  * moe_pack_weights and the quantisers read the result).  With t = *step + 1:
  *   g = grad * grad_scale;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
  *   p = p - lr (wd p + (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
- * in fp32 (a v below fp32's normal range has the root 0).  `tensors` is a HOST array of `count` entries, read during the
- * call; the addresses in it are device pointers and travel as kernel
- * arguments, so the call may be captured.
+ * in fp32 (a v below fp32's normal range has the root 0).  `tensors` is a HOST
+ * array of `count` entries, read during the call; the addresses in it are device
+ * pointers and travel as kernel arguments, so the call may be captured.
  *   param    bf16 or fp32 (param_dtype) [n]
  *   master   fp32 [n] copy that the step works on; param (bf16) receives it
  *            rounded to nearest.  All entries have one or none has; with

@@ -109,6 +109,23 @@ int main() {
   check(g_launches == before, "nothing launched");
   check(moe_gated_ffn(u16(P), 64, u16(P), u16(P), nullptr, 0, INT32_MAX, 64, 64, nullptr, nullptr, u16(2 * P), ws, SIZE_MAX,
                       nullptr) == MOE_OK, "ffn, largest T");
+  // in place, the rows read and written must be the same ones
+  const int placed = g_launches;
+  check(moe_add_rmsnorm(u16(P), 64, u16(P), 0, u16(2 * P), 0, 80, u16(2 * P), 64, 4, 64, 1e-6f, u16(3 * P), nullptr,
+                        nullptr, nullptr, nullptr) == MOE_ERR_INVALID_ARG, "s in r's place, another pitch");
+  check(moe_add_rmsnorm(u16(P), 80, u16(P), 0, u16(2 * P), 0, 64, u16(P), 64, 4, 64, 1e-6f, u16(3 * P), nullptr, nullptr,
+                        nullptr, nullptr) == MOE_ERR_INVALID_ARG, "s in x's place, another pitch");
+  check(moe_add_rmsnorm_backward(u16(P), 80, u16(2 * P), 0, 64, u16(P), 0, (float*)P, nullptr, 0, 4, 64, u16(P), nullptr,
+                                 (float*)P, ws, SIZE_MAX, nullptr) == MOE_ERR_INVALID_ARG, "dx in dy's place");
+  check(g_launches == placed, "nothing launched in place");
+  check(moe_add_rmsnorm(u16(P), 64, u16(P), 0, u16(2 * P), 0, 80, u16(2 * P), 80, 4, 64, 1e-6f, u16(3 * P), nullptr,
+                        nullptr, nullptr, nullptr) == MOE_OK, "s in r's place");
+  check(moe_add_rmsnorm_backward(u16(P), 64, u16(2 * P), 0, 64, u16(P), 0, (float*)P, nullptr, 0, 4, 64, u16(P), nullptr,
+                                 (float*)P, ws, SIZE_MAX, nullptr) == MOE_OK, "dx in dy's place");
+  // workgroup numbers past one launch dimension
+  for (int64_t n : {(int64_t)1, moe::kGridX - 1, moe::kGridX, moe::kGridX + 1, (int64_t)INT32_MAX})
+    check(moe::grid_x(n) * moe::grid_y(n) >= n && moe::grid_x(n) * moe::grid_y(n) - n < moe::kGridX &&
+              moe::grid_x(n) * 1024 < ((int64_t)1 << 32) && moe::grid_y(n) <= 65535, "grid");
   adamw_lists({});
   adamw_lists({0, 0});
   adamw_lists({1});

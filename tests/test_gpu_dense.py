@@ -676,6 +676,86 @@ def test_adamw_past_32_bit_elements(ops):
                  r[skip:] & np.uint64(0xFFFF), "m codes")
 
 
+def _some_rows(T, n=4096):
+    """Rows at both ends and around the 2^20 workgroups that one launch dimension takes."""
+    return torch.cat([torch.arange(0, n), torch.arange(T - n, T)]).cuda()
+
+
+@pytest.mark.parametrize("d,rows", [(1, 32), (8, 32), (9000, 1)])
+def test_norm_of_more_workgroups_than_one_dimension(ops, d, rows):
+    """rows: of a workgroup."""
+    T = (1 << 20) * rows + 4095
+    if d == 9000:
+        T = (1 << 20) + 130
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randint(-8, 9, (T, d), generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    w = _t(np.random.default_rng(31), (d,))
+    say("norm workgroups", T, d)
+    o = ops.add_rmsnorm(x, w, keep_rstd=True)
+    at = _some_rows(T, 4096 if d < 100 else 100)
+    y, rstd = o["y"][at], o["rstd"][at]
+    S = f64(x[at])
+    k = 1 / np.sqrt((S * S).mean(1) + 1e-6)
+    # the sum of squares of integers is exact; division, sum, root and reciprocal: four roundings and the hardware's
+    _within(rstd, k, 16 * ULP32 * k, "rstd")
+    ref = S * k[:, None] * f64(w)
+    _within(y, ref, (ULP16 + 20 * ULP32) * np.abs(ref) * (1 + ULP16) + 2.0 ** -126, "y")
+
+
+def test_ffn_of_more_workgroups_than_one_dimension(ops):
+    T, d, f = (1 << 28) + 300, 8, 8      # 2^20 + 2 tiles of 256 rows
+    rng = np.random.default_rng(32)
+    w1, w2 = _t(rng, (2 * f, d), scale=d ** -0.5), _t(rng, (d, f), scale=f ** -0.5)
+    x = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    at = _some_rows(T)
+    x[at] = _t(rng, (len(at), d))
+    say("ffn workgroups", T)
+    y = ops.gated_ffn(x, w1, w2)
+    small, kept = ops.gated_ffn(x[at], w1, w2, keep=True)
+    _, h, _ = R.ffn(f64(x[at]), f64(w1), f64(w2))
+    # one stage of K in either call, in one order: the same sums
+    _bits_equal(y[at], small, "y")
+    H = f64(kept["h"])
+    ref = H @ f64(w2).T
+    _within(small, ref, ULP16 * np.abs(ref) + 1.01 * (f + 2) * ULP32 * (np.abs(H) @ np.abs(f64(w2)).T) + 2.0 ** -126, "y")
+    assert not y[4096:-4096].any()
+
+
+def test_ffn_backward_of_more_workgroups_than_one_dimension(ops):
+    T, d, f = (1 << 27) + 300, 8, 8      # 2^20 + 3 tiles of 128 rows for dx alone
+    rng = np.random.default_rng(33)
+    w1, w2 = _t(rng, (2 * f, d), scale=d ** -0.5), _t(rng, (d, f), scale=f ** -0.5)
+    zeros = lambda n: torch.zeros((T, n), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    x, dy, saved = zeros(d), zeros(d), dict(h=zeros(f), gu=zeros(2 * f))
+    at = _some_rows(T)
+    cut_x, cut_dy = _t(rng, (len(at), d)), _t(rng, (len(at), d))
+    _, cut = ops.gated_ffn(cut_x, w1, w2, keep=True)
+    x[at], dy[at], saved["h"][at], saved["gu"][at] = cut_x, cut_dy, cut["h"], cut["gu"]
+    say("ffn backward workgroups", T)
+    o = ops.gated_ffn_backward(dy, x, saved, w1, w2, out_dtype=torch.float32)
+    p = ops.gated_ffn_backward(cut_dy, cut_x, cut, w1, w2, out_dtype=torch.float32)
+    for k in ("dgu", "dx"):
+        _bits_equal(o[k][at], p[k], k)
+        assert not o[k][4096:-4096].any(), k
+    # rows of zeros add nothing: 8192 terms, in whatever order
+    G = f64(p["dgu"])
+    for k, (a, b) in dict(dw1p=(G, f64(cut_x)), dw2=(f64(cut_dy), f64(cut["h"]))).items():
+        _within(o[k], a.T @ b, len(at) * ULP32 * (np.abs(a).T @ np.abs(b)), k)
+
+
+def test_in_place_norm_refuses_other_rows(ops):
+    """In place, the rows read and written are the same ones."""
+    buf = torch.zeros(4 * 80, dtype=torch.bfloat16, device="cuda")
+    x, w = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda"), torch.ones(64, device="cuda")
+    r = buf.as_strided((4, 64), (80, 1))
+    with pytest.raises(ops.MoeError):
+        ops.add_rmsnorm(x, w, r, out_s=buf.as_strided((4, 64), (64, 1)))
+    with pytest.raises(ops.MoeError):
+        ops.add_rmsnorm(r, w, x, out_s=buf.as_strided((4, 64), (72, 1)))
+    ops.add_rmsnorm(x, w, r, out_s=r)
+    ops.add_rmsnorm(r, w, x, out_s=r)
+
+
 # ------------------------------------------------------------------ as they are used
 
 def _replayed(make, run, outputs, other):
