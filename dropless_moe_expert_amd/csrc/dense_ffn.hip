@@ -580,9 +580,9 @@ struct Plan {
 };
 
 // What the forms cost, in microseconds; only their order matters.  Constants
-// fitted to 102 sizes (three of the products, 17 to 4096 tokens, widths 768 to
-// 14336, every tile height and split) timed on MI355X: the choice they lead to
-// is 0.7 % from the best one on average, 8 % at most.  A stage (64 deep) of a
+// fitted to sizes timed on MI355X; on 119 of them (three of the products, 17 to
+// 4096 tokens, widths 768 to 14336, every tile height and split) the choice they
+// lead to is 0.7 % from the best one on average, 8 % at most.  A stage (64 deep) of a
 // 128 x 128 tile takes 0.60 with K contiguous, 0.78 with a K-outer operand
 // (two: 0.85, from the backward's second launch), of a 64 or 256 x 128 tile 0.67
 // or 1.72 of that; down to 0.68 of it where the tiles do not fill the chip.  A
